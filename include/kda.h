@@ -50,7 +50,8 @@
  * by the caller (same stream or events).
  *
  * Supported sizes: dk, dv in {64, 128}; B >= 0 (B = 0 is a no-op); H >= 1;
- * verify 1 <= T <= T_max <= 16; prefill chunk in {32, 64}.
+ * verify 1 <= T <= T_max <= 16; prefill chunk in {32, 64}.  The paged
+ * attention calls have shapes of their own (kda_kv_shape).
  */
 #ifndef KDA_H
 #define KDA_H
@@ -75,7 +76,11 @@ typedef enum kda_status {
   KDA_ERR_HIP = 7     /* the HIP runtime rejected a launch */
 } kda_status;
 
-typedef enum kda_dtype { KDA_BF16 = 0, KDA_F32 = 1 } kda_dtype;
+typedef enum kda_dtype {
+  KDA_BF16 = 0,
+  KDA_F32 = 1,
+  KDA_E4M3 = 2 /* 8-bit floats (4 exponent, 3 mantissa bits, no infinity): cache_dtype of kda_kv_shape only */
+} kda_dtype;
 
 /* Bits set in the device error word. */
 #define KDA_DEV_ERR_ACCEPTED 1 /* an accepted count was outside [0, T] */
@@ -83,6 +88,9 @@ typedef enum kda_dtype { KDA_BF16 = 0, KDA_F32 = 1 } kda_dtype;
 #define KDA_DEV_ERR_DRAFT_LEN 4 /* a per-sequence draft length was outside [0, T] */
 #define KDA_DEV_ERR_SLOT_ID 8   /* a device-side state slot id was outside [0, n_slots) */
 #define KDA_DEV_ERR_MIXED 16    /* kda_mixed_step: roles or token ranges inconsistent with the launch */
+#define KDA_DEV_ERR_PAGE 32     /* a page id outside [0, n_pages), or a position past the page table */
+#define KDA_DEV_ERR_POS 64      /* kda_kv_append: a position below 0 or past the rotation table */
+#define KDA_DEV_ERR_TOKENS 128  /* kda_kv_append, kda_attn_decode: a token range inconsistent with the launch */
 
 /* Kernel variants reported by kda_last_variant(). */
 #define KDA_VARIANT_NONE 0
@@ -108,6 +116,8 @@ typedef enum kda_dtype { KDA_BF16 = 0, KDA_F32 = 1 } kda_dtype;
 #define KDA_VARIANT_COMMIT_VERIFY_SLOTS 20
 #define KDA_VARIANT_PREFILL_CHUNKED_SLOTS 21
 #define KDA_VARIANT_MIXED 22
+#define KDA_VARIANT_KV_APPEND 23
+#define KDA_VARIANT_ATTN_DECODE 24
 
 /* What a sequence does in a kda_mixed_step. */
 #define KDA_ROLE_IDLE 0    /* nothing this step */
@@ -490,6 +500,132 @@ kda_status kda_mixed_step(const kda_shape* shape, const int32_t* roles, const in
                           const int32_t* slot_ids, int32_t n_slots, const void* q, const void* k, const void* v,
                           const float* alpha, const float* beta, float* o, kda_log* log, const int32_t* accepted,
                           int32_t* dev_err, void* stream);
+
+/*
+ * The paged attention cache of the attention layers that alternate with the
+ * recurrent ones (webinar summary: a recurrent state next to an attention
+ * cache that grows with the sequence, the two allocated and reused in their
+ * own ways and cut at the same token boundary).  Both calls below take the
+ * positions `pos` that the recurrent calls advance, read them and leave them
+ * as they are: append and attend with the pos of before the round, then let
+ * the recurrent decode or commit advance it.  Rejected drafts need no
+ * clean-up: the next append writes over them and no query sees past its own
+ * position.
+ *
+ * Two forms:
+ *   grouped  dk == dv in {64, 128}; Hq / Hkv query heads share a kv head.
+ *            in_dtype KDA_BF16 with cache_dtype KDA_BF16 or KDA_E4M3, or
+ *            both KDA_F32.
+ *   latent   dk = 576, dv = 512, Hkv = 1, both types KDA_BF16: one row per
+ *            token that all query heads share.  The row is the key and its
+ *            first dv values are the value; there are no value pages
+ *            (kda_pages.v and every `v` argument are NULL).
+ *
+ * Tokens: with tok_start NULL every sequence brings T tokens and rows are
+ * [B][T] (n_tokens must be B * T).  Otherwise tok_start is a device int32
+ * [B + 1] as in kda_mixed_step: sequence b's tokens are the packed rows
+ * tok_start[b] .. tok_start[b + 1] - 1 of n_tokens, at most T of them (0:
+ * the sequence sits the call out).  Token i of sequence b has position
+ * pos[b] + i.  A range that is outside [0, n_tokens], runs backwards or is
+ * longer than T sets KDA_DEV_ERR_TOKENS in *dev_err and the sequence is
+ * skipped (nothing of it is written).  Rows of no sequence are left as they
+ * are.
+ */
+typedef struct kda_kv_shape {
+  int32_t B;           /* sequences in the batch */
+  int32_t T;           /* most new tokens of a sequence in this call */
+  int32_t Hq;          /* query heads, a multiple of Hkv */
+  int32_t Hkv;         /* key/value heads */
+  int32_t dk;          /* key and query width */
+  int32_t dv;          /* value width */
+  int32_t in_dtype;    /* kda_dtype of q, k, v and o */
+  int32_t cache_dtype; /* kda_dtype of the pages */
+} kda_kv_shape;
+
+/*
+ * Page pool, caller-owned device memory:
+ *   k  cache_dtype [n_pages][Hkv][page_size][dk]
+ *   v  cache_dtype [n_pages][Hkv][page_size][dv]   (NULL in the latent form)
+ *   k_scale, v_scale  f32 [Hkv], KDA_E4M3 only (otherwise ignored): the pages
+ *      hold value / scale
+ * page_size is a power of two in [16, 1024].  The pools must be 16-byte
+ * aligned.  A page table is a device int32 [B][max_pages]: entry i of
+ * sequence b is the page with its tokens i * page_size and on; entries past
+ * the tokens in use are not read.  max_pages * page_size <= 2^30.
+ */
+typedef struct kda_pages {
+  void* k;
+  void* v;
+  const float* k_scale;
+  const float* v_scale;
+  int32_t n_pages;
+  int32_t page_size;
+} kda_pages;
+
+/*
+ * Position rotation of values start .. start + dim - 1 of every head
+ * (start and dim multiples of 16): the pair (x_i, x_j) at position p becomes
+ * (x_i c - x_j s, x_j c + x_i s) with c = cos_sin[p][n], s =
+ * cos_sin[p][dim / 2 + n] for the n-th pair, (i, j) = (n, dim / 2 + n), or
+ * (2n, 2n + 1) when `pairs` is not 0, counted from `start`.  Computed in fp32
+ * and rounded once.  cos_sin: f32 [max_pos][dim], 16-byte aligned.
+ */
+typedef struct kda_rotation {
+  const float* cos_sin;
+  int32_t max_pos;
+  int32_t start;
+  int32_t dim;
+  int32_t pairs;
+} kda_rotation;
+
+/*
+ * Append: the new tokens' keys (in_dtype rows of [Hkv][dk]), rotated, and
+ * values (rows of [Hkv][dv]) go to their places in the pages; the queries
+ * (rows of [Hq][dk]) are rotated into q_out in the same launch.  A row of
+ * k, v, q or q_out starts *_stride elements after the one before (0: dense),
+ * so all three can be slices of one projection; strides keep rows 16-byte
+ * aligned.  q and q_out are both given or both NULL; q_out may be q itself
+ * with its stride.  `rot` NULL stores keys as they are (q must be NULL then).
+ * KDA_E4M3 pages get x / scale, clamped to +-448 and rounded to nearest even
+ * (NaN stays NaN).  A token whose position is below 0 or past the rotation
+ * table (KDA_DEV_ERR_POS), or past the page table or on a page outside
+ * [0, n_pages) (KDA_DEV_ERR_PAGE), is skipped, its q_out row included.  Two
+ * tokens of one call must not share a place (sequences may share pages of a
+ * common prefix, which no call writes).  dev_err must not be NULL.
+ */
+kda_status kda_kv_append(const kda_kv_shape* shape, const kda_pages* pages, const int32_t* table, int32_t max_pages,
+                         const int32_t* tok_start, int32_t n_tokens, const int64_t* pos, const void* k,
+                         int64_t k_stride, const void* v, int64_t v_stride, const void* q, int64_t q_stride,
+                         void* q_out, int64_t q_out_stride, const kda_rotation* rot, int32_t* dev_err, void* stream);
+
+/*
+ * Attention of the new tokens over the cache: query row r at position p
+ * (in_dtype [Hq][dk], q_stride as above) sees the cached tokens j with
+ * max(0, p - window + 1) <= j <= p (window 0: no lower bound) and gets
+ *   o = sum_j e^(s_j) v_j / sum_j e^(s_j),  s_j = scale (q . k_j)
+ * as in_dtype o [n_tokens][Hq][dv], and, when lse is not NULL, f32
+ * lse [n_tokens][Hq] = log sum_j e^(s_j).  Its own key and value are read from
+ * the cache, so they are appended first.  A row that sees no token (p < 0)
+ * gets o = 0 and lse = -inf.  Tokens that a row does not see do not reach it,
+ * whatever they hold.  1 <= T <= 16 (a decode token, or the drafts of a
+ * speculative round).  scale normally 1/sqrt of the width the model trained
+ * with; it must be finite.
+ * A sequence whose visible tokens run past the page table or lie on a page
+ * outside [0, n_pages) sets KDA_DEV_ERR_PAGE and is skipped.
+ * workspace: kda_attn_workspace_bytes(shape, pages, max_pages) bytes of
+ * device memory, 256-byte aligned, holding nothing between calls; calls that
+ * may run at the same time need one each.  The cache's split over the chip
+ * depends on the positions only, so equal calls give equal bits.
+ * (vLLM blog, Part 1, section 2: decode attention whose cache is split, and
+ * whose partial results one kernel combines.)
+ */
+kda_status kda_attn_decode(const kda_kv_shape* shape, const kda_pages* pages, const int32_t* table,
+                           int32_t max_pages, const int32_t* tok_start, int32_t n_tokens, const int64_t* pos,
+                           const void* q, int64_t q_stride, float scale, int32_t window, void* o, float* lse,
+                           void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream);
+
+/* Bytes of kda_attn_decode's workspace; 0 for an invalid shape. */
+size_t kda_attn_workspace_bytes(const kda_kv_shape* shape, const kda_pages* pages, int32_t max_pages);
 
 /* Human-readable name of a status code (static string). */
 const char* kda_status_str(kda_status status);

@@ -17,15 +17,16 @@ import torch  # loads the HIP runtime that libkda then shares (same soname)
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkda.so")
 
-KDA_BF16, KDA_F32 = 0, 1
+KDA_BF16, KDA_F32, KDA_E4M3 = 0, 1, 2
 VARIANTS = {0: "none", 1: "decode", 2: "verify", 3: "commit", 4: "snapshot", 5: "restore",
             6: "prefill_recurrent", 7: "prefill_chunked", 8: "commit_verify", 9: "verify_varlen",
             10: "commit_verify_varlen", 11: "decode_prep", 12: "verify_prep", 13: "commit_verify_prep",
             14: "decode_slots", 15: "slot_copy", 16: "prefill_chunked_prep", 17: "prefill_recurrent_prep",
             18: "verify_slots", 19: "commit_slots", 20: "commit_verify_slots", 21: "prefill_chunked_slots",
-            22: "mixed"}
+            22: "mixed", 23: "kv_append", 24: "attn_decode"}
 GATE_EXP_NEG_SOFTPLUS, GATE_SIGMOID = 0, 1
 DEV_ERR_ACCEPTED, DEV_ERR_CKPT_SLOT, DEV_ERR_DRAFT_LEN, DEV_ERR_SLOT_ID, DEV_ERR_MIXED = 1, 2, 4, 8, 16
+DEV_ERR_PAGE, DEV_ERR_POS, DEV_ERR_TOKENS = 32, 64, 128
 ROLE_IDLE, ROLE_DECODE, ROLE_SPEC, ROLE_PREFILL = 0, 1, 2, 3
 
 
@@ -49,10 +50,25 @@ class _Slots(ctypes.Structure):
     _fields_ = [("states", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("n_slots", ctypes.c_int32)]
 
 
+class KvShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "Hq", "Hkv", "dk", "dv", "in_dtype", "cache_dtype")]
+
+
+class _Pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class _Rotation(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_pos", ctypes.c_int32), ("start", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("pairs", ctypes.c_int32)]
+
+
 _lib = None
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_L = ctypes.c_int64
 _SIGS = {
     "kda_log_bytes": (ctypes.c_size_t, [ctypes.POINTER(Shape), _I]),
     "kda_slot_bytes": (ctypes.c_size_t, [ctypes.POINTER(Shape)]),
@@ -91,6 +107,11 @@ _SIGS = {
                                         ctypes.POINTER(_Slots), _P, _P]),
     "kda_mixed_step": (_I, [ctypes.POINTER(Shape), _P, _P, _I, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P,
                             ctypes.POINTER(_Log), _P, _P, _P]),
+    "kda_kv_append": (_I, [ctypes.POINTER(KvShape), ctypes.POINTER(_Pages), _P, _I, _P, _I, _P, _P, _L, _P, _L, _P, _L,
+                           _P, _L, ctypes.POINTER(_Rotation), _P, _P]),
+    "kda_attn_decode": (_I, [ctypes.POINTER(KvShape), ctypes.POINTER(_Pages), _P, _I, _P, _I, _P, _P, _L,
+                             ctypes.c_float, _I, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "kda_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(KvShape), ctypes.POINTER(_Pages), _I]),
     "kda_status_str": (ctypes.c_char_p, [_I]),
     "kda_last_variant": (_I, []),
     "kda_abi_version": (_I, []),
@@ -666,3 +687,225 @@ class CommitVerifyPlan:
 
     def __call__(self):
         _check(self._fn(*self._args, _stream()))
+
+
+_DTYPE_CODES = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32, torch.float8_e4m3fn: KDA_E4M3}
+
+
+class PagePool:
+    """Caller-owned pages of the attention cache: k [n_pages][Hkv][page_size][dk], v [n_pages][Hkv][page_size][dv].
+
+    `latent` pools have no v: a row's first dv values are its value.  An e4m3
+    pool (dtype torch.float8_e4m3fn) holds value / scale, with one f32 scale
+    per kv head in k_scale and v_scale.
+    """
+
+    def __init__(self, n_pages: int, page_size: int, Hkv: int, dk: int, dv: int, device, dtype=torch.bfloat16,
+                 latent: bool = False, k_scale=None, v_scale=None):
+        k = torch.zeros((n_pages, Hkv, page_size, dk), dtype=dtype, device=device)
+        v = None if latent else torch.zeros((n_pages, Hkv, page_size, dv), dtype=dtype, device=device)
+        self._hold(k, v, dv, k_scale, v_scale)
+
+    @classmethod
+    def from_tensors(cls, k, v=None, *, dv=None, k_scale=None, v_scale=None) -> "PagePool":
+        """A pool over existing tensors (v None: latent, dv its value width)."""
+        pool = cls.__new__(cls)
+        if v is None and dv is None:
+            raise ValueError("a latent pool needs its value width dv")
+        pool._hold(k, v, v.shape[-1] if v is not None else int(dv), k_scale, v_scale)
+        return pool
+
+    def _hold(self, k, v, dv, k_scale, v_scale):
+        if k.dim() != 4:
+            raise ValueError(f"k has shape {tuple(k.shape)}, expected [n_pages][Hkv][page_size][dk]")
+        n_pages, Hkv, page_size, dk = k.shape
+        if k.dtype not in _DTYPE_CODES:
+            raise TypeError(f"page dtype must be bfloat16, float32 or float8_e4m3fn, not {k.dtype}")
+        _need_gpu(k, "k")
+        _need(k, "k", k.shape, k.dtype, k.device)
+        if v is not None:
+            _need(v, "v", (n_pages, Hkv, page_size, dv), k.dtype, k.device)
+        if k.dtype == torch.float8_e4m3fn:
+            _need(k_scale, "k_scale", (Hkv,), torch.float32, k.device)
+            _need(v_scale, "v_scale", (Hkv,), torch.float32, k.device)
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("scales belong to float8_e4m3fn pages only")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.Hkv, self.page_size, self.dk = n_pages, Hkv, page_size, dk
+        self.dv, self.latent, self.device = dv, v is None, k.device
+        self.c = _Pages(*(None if x is None else x.data_ptr() for x in (k, v, k_scale, v_scale)), n_pages, page_size)
+
+
+def _need_gpu(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} is on {t.device}: the library reads device memory")
+
+
+def _launch_on(device, fn, args):
+    """Calls fn on the current stream of the tensors' device."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch_on(device, fn, args)
+    _check(fn(*args, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)))
+
+
+def _kv_shape(pool: PagePool, table, pos, Hq, T, in_dtype, tok_start):
+    if in_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"token dtype must be bfloat16 or float32, not {in_dtype}")
+    if table.dim() != 2:
+        raise ValueError(f"table has shape {tuple(table.shape)}, expected [B][max_pages]")
+    B, max_pages = table.shape
+    _need(table, "table", (B, max_pages), torch.int32, pool.device)
+    if pos is not None:
+        _need(pos, "pos", (B,), torch.int64, pool.device)
+    if tok_start is not None:
+        _need(tok_start, "tok_start", (B + 1,), torch.int32, pool.device)
+    return KvShape(B, T, Hq, pool.Hkv, pool.dk, pool.dv, _DTYPE_CODES[in_dtype], _DTYPE_CODES[pool.k.dtype])
+
+
+def _rows(t, name, B, T, width, dtype, device, tok_start, heads=None):
+    """Token rows [B][T][heads][width] (or [N][heads][width] with tok_start), each row dense and the rows evenly
+    spaced: (heads, rows, stride in elements)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    lead = 1 if tok_start is not None else 2
+    if t.dim() != lead + 2 or t.shape[-1] != width or (heads is not None and t.shape[-2] != heads) or \
+            (lead == 2 and tuple(t.shape[:2]) != (B, T)):
+        want = f"[N][{heads or 'heads'}][{width}]" if lead == 1 else f"[{B}][{T}][{heads or 'heads'}][{width}]"
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {want}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    H = t.shape[-2]
+    rows = t.shape[0] if lead == 1 else B * T
+    # The distance of neighbouring rows; a length-1 axis has no say.
+    if rows <= 1:
+        stride = H * width
+    elif lead == 1 or T == 1:
+        stride = t.stride(0)
+    else:
+        stride = t.stride(1)
+        if B > 1 and t.stride(0) != T * stride:
+            raise ValueError(f"{name}: the rows of one sequence must follow those of the one before")
+    if (width > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != width) or (rows > 1 and stride < H * width):
+        raise ValueError(f"{name}: the values of a row must be dense")
+    return H, rows, stride
+
+
+def _packed_T(t, tok_start, T, name):
+    """T of a call: given for packed rows, the tensor's own otherwise."""
+    if tok_start is None:
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be [B][T][heads][width] without tok_start")
+        if T is not None and T != t.shape[1]:
+            raise ValueError(f"T is {T}, but {name} brings {t.shape[1]} tokens to each sequence")
+        return t.shape[1]
+    if T is None:
+        raise ValueError("packed rows need T, the most tokens of a sequence")
+    return int(T)
+
+
+class KvAppendPlan:
+    """A kv_append call validated once (see DecodePlan)."""
+
+    def __init__(self, pool: PagePool, table, pos, k, v, dev_err, *, q=None, q_out=None, cos_sin=None, rot_start=0,
+                 rot_pairs=False, tok_start=None, T=None):
+        dev, dt = pool.device, k.dtype
+        T = _packed_T(k, tok_start, T, "k")
+        sh = _kv_shape(pool, table, pos, 1 if q is None else q.shape[-2], T, dt, tok_start)
+        _need(dev_err, "dev_err", (1,), torch.int32, dev)
+        if (v is None) != pool.latent:
+            raise ValueError("values go with pools that have value pages, and only those")
+        if (q is None) != (q_out is None):
+            raise ValueError("q and q_out belong together")
+        if q is not None and cos_sin is None:
+            raise ValueError("queries are only rotated: q needs cos_sin")
+        if q is None:
+            sh.Hq = sh.Hkv
+        _, N, ks = _rows(k, "k", sh.B, T, pool.dk, dt, dev, tok_start, pool.Hkv)
+        vs = qs = qos = 0
+        if v is not None:
+            vs = _rows(v, "v", sh.B, T, pool.dv, dt, dev, tok_start, pool.Hkv)
+        if q is not None:
+            qs = _rows(q, "q", sh.B, T, pool.dk, dt, dev, tok_start)
+            qos = _rows(q_out, "q_out", sh.B, T, pool.dk, dt, dev, tok_start, q.shape[-2])
+        for name, r in (("v", vs), ("q", qs), ("q_out", qos)):
+            if r and r[1] != N:
+                raise ValueError(f"{name} has {r[1]} rows, k has {N}")
+        vs, qs, qos = (r[2] if r else 0 for r in (vs, qs, qos))
+        rot = None
+        if cos_sin is not None:
+            if cos_sin.dim() != 2:
+                raise ValueError(f"cos_sin has shape {tuple(cos_sin.shape)}, expected [max_pos][rotated values]")
+            _need(cos_sin, "cos_sin", cos_sin.shape, torch.float32, dev)
+            rot = _Rotation(cos_sin.data_ptr(), cos_sin.shape[0], int(rot_start), cos_sin.shape[1], int(rot_pairs))
+        self._keep = (pool, table, pos, k, v, q, q_out, cos_sin, tok_start, dev_err, sh, rot)
+        self._device = dev
+        self._args = (ctypes.byref(sh), ctypes.byref(pool.c), _ptr(table), table.shape[1], _ptr(tok_start), N,
+                      _ptr(pos), _ptr(k), ks, _ptr(v), vs, _ptr(q), qs, _ptr(q_out), qos,
+                      None if rot is None else ctypes.byref(rot), _ptr(dev_err))
+        self._fn = lib().kda_kv_append
+
+    def __call__(self):
+        _launch_on(self._device, self._fn, self._args)
+
+
+def kv_append(pool: PagePool, table, pos, k, v, dev_err, **kw):
+    """Append new tokens' keys (rotated) and values to the paged cache, and rotate their queries into q_out.
+
+    Rows are [B][T][heads][width], or packed [N][heads][width] with tok_start
+    (device int32 [B + 1]) and T, the most tokens of a sequence; they may be
+    slices of one projection.  cos_sin: f32 [max_pos][rotated values], cosines
+    then sines, rotating the values from rot_start on (rot_pairs: neighbours
+    form the pairs, else halves).  Keywords: q, q_out, cos_sin, rot_start,
+    rot_pairs, tok_start, T.
+    """
+    KvAppendPlan(pool, table, pos, k, v, dev_err, **kw)()
+
+
+def attn_workspace(pool: PagePool, table, *, Hq: int, T: int = 1):
+    """A workspace for attn_decode calls with this pool, table shape, query heads and up to T new tokens."""
+    sh = _kv_shape(pool, table, None, Hq, T, torch.float32 if pool.k.dtype == torch.float32 else torch.bfloat16, None)
+    n = int(lib().kda_attn_workspace_bytes(ctypes.byref(sh), ctypes.byref(pool.c), table.shape[1]))
+    if n == 0:
+        raise ValueError("unsupported attention shape")
+    return torch.empty(n, dtype=torch.uint8, device=pool.device)
+
+
+class AttnDecodePlan:
+    """An attn_decode call validated once (see DecodePlan)."""
+
+    def __init__(self, pool: PagePool, table, pos, q, o, workspace, dev_err, *, lse=None, scale=None, window=0,
+                 tok_start=None, T=None):
+        dev, dt = pool.device, q.dtype
+        T = _packed_T(q, tok_start, T, "q")
+        sh = _kv_shape(pool, table, pos, q.shape[-2], T, dt, tok_start)
+        Hq, N, qs = _rows(q, "q", sh.B, T, pool.dk, dt, dev, tok_start)
+        lead = (N,) if tok_start is not None else (sh.B, T)
+        _need(o, "o", lead + (Hq, pool.dv), dt, dev)
+        if lse is not None:
+            _need(lse, "lse", lead + (Hq,), torch.float32, dev)
+        _need(dev_err, "dev_err", (1,), torch.int32, dev)
+        _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+        self._keep = (pool, table, pos, q, o, workspace, lse, tok_start, dev_err, sh)
+        self._device = dev
+        self._args = (ctypes.byref(sh), ctypes.byref(pool.c), _ptr(table), table.shape[1], _ptr(tok_start), N,
+                      _ptr(pos), _ptr(q), qs, float(pool.dk) ** -0.5 if scale is None else float(scale), int(window),
+                      _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(dev_err))
+        self._fn = lib().kda_attn_decode
+
+    def __call__(self):
+        _launch_on(self._device, self._fn, self._args)
+
+
+def attn_decode(pool: PagePool, table, pos, q, o, workspace, dev_err, **kw):
+    """Attention of the new tokens' queries over the paged cache, up to and including their own positions.
+
+    q, o: [B][T][Hq][width], or packed [N][Hq][width] with tok_start and T;
+    lse (optional): f32, o's shape without the width.  window: the tokens that a
+    query sees (0: all).  Keywords: lse, scale, window, tok_start, T.
+    """
+    AttnDecodePlan(pool, table, pos, q, o, workspace, dev_err, **kw)()

@@ -120,6 +120,65 @@ kda_status check_pairs(const kda_shape& s, const int32_t* seq_ids, const int32_t
   return KDA_OK;
 }
 
+// The paged attention calls (kda_kv_append, kda_attn_decode).
+bool is_latent(const kda_kv_shape& s) { return s.dk == 576 && s.dv == 512; }
+
+kda_status check_kv_shape(const kda_kv_shape* s, const kda_pages* pages, int32_t max_pages) {
+  if (!s || !pages) return KDA_ERR_NULL;
+  if (s->in_dtype != KDA_BF16 && s->in_dtype != KDA_F32) return KDA_ERR_DTYPE;
+  if (s->cache_dtype != s->in_dtype && !(s->in_dtype == KDA_BF16 && s->cache_dtype == KDA_E4M3)) return KDA_ERR_DTYPE;
+  if (s->B < 0 || s->T < 1 || s->Hkv < 1 || s->Hq < 1 || s->Hq % s->Hkv != 0 || s->Hq > 4096) return KDA_ERR_SHAPE;
+  if (is_latent(*s)) {
+    if (s->Hkv != 1) return KDA_ERR_SHAPE;
+    if (s->cache_dtype != KDA_BF16) return KDA_ERR_DTYPE;
+  } else if (s->dk != s->dv || !(s->dk == 64 || s->dk == 128)) {
+    return KDA_ERR_SHAPE;
+  }
+  const int32_t ps = pages->page_size;
+  if (ps < 16 || ps > 1024 || (ps & (ps - 1)) != 0 || pages->n_pages < 0 || max_pages < 1) return KDA_ERR_SHAPE;
+  if ((int64_t)max_pages * ps > (int64_t)1 << 30) return KDA_ERR_SHAPE;
+  if ((int64_t)s->B * s->T > (int64_t)1 << 30) return KDA_ERR_SHAPE;
+  return KDA_OK;
+}
+
+// Everything the two calls share; fills in `b` on success.
+kda_status check_kv(const kda_kv_shape* s, const kda_pages* pages, const int32_t* table, int32_t max_pages,
+                    const int32_t* tok_start, int32_t n_tokens, const int64_t* pos, int32_t* dev_err,
+                    kda::KvBatch* b) {
+  kda_status r = check_kv_shape(s, pages, max_pages);
+  if (r != KDA_OK) return r;
+  if (n_tokens < 0 || n_tokens > 1 << 30) return KDA_ERR_SHAPE;
+  if (!tok_start && (int64_t)n_tokens != (int64_t)s->B * s->T) return KDA_ERR_SHAPE;
+  // A grid of one 256-thread block per 256 units of 16 values must fit.
+  const int64_t units = ((int64_t)s->Hq * s->dk + (int64_t)s->Hkv * (s->dk + s->dv)) / 16;
+  if ((int64_t)n_tokens * units > (int64_t)1 << 38) return KDA_ERR_SHAPE;
+  if (s->B > 0 && n_tokens > 0) {
+    const bool latent = is_latent(*s);
+    if (!table || !pos || !dev_err || !pages->k || (!latent && !pages->v)) return KDA_ERR_NULL;
+    if (latent && pages->v) return KDA_ERR_SHAPE;
+    if (s->cache_dtype == KDA_E4M3 && (!pages->k_scale || !pages->v_scale)) return KDA_ERR_NULL;
+    if (!aligned(table, 4) || !aligned(pos, 8) || !aligned(dev_err, 4) || !aligned(pages->k, 16) ||
+        !aligned(pages->v, 16) || !aligned(tok_start, 4))
+      return KDA_ERR_ALIGN;
+    if (s->cache_dtype == KDA_E4M3 && (!aligned(pages->k_scale, 4) || !aligned(pages->v_scale, 4)))
+      return KDA_ERR_ALIGN;
+  }
+  int32_t shift = 0;
+  while ((1 << shift) < pages->page_size) ++shift;
+  *b = kda::KvBatch{*s, *pages, table, max_pages, shift, tok_start, n_tokens, pos, dev_err};
+  if (s->cache_dtype != KDA_E4M3) b->pages.k_scale = b->pages.v_scale = nullptr;
+  return KDA_OK;
+}
+
+// Token rows of `heads` x `width` in_dtype values: a stride of 0 becomes the
+// dense one; others must hold a row and keep rows 16-byte aligned.
+kda_status check_rows(const kda_kv_shape& s, int32_t heads, int32_t width, kda::KvRows* rows) {
+  const int64_t dense = (int64_t)heads * width, per16 = s.in_dtype == KDA_BF16 ? 8 : 4;
+  if (rows->stride == 0) rows->stride = dense;
+  if (rows->stride < dense || rows->stride > (int64_t)1 << 32) return KDA_ERR_SHAPE;
+  return rows->stride % per16 == 0 ? KDA_OK : KDA_ERR_ALIGN;
+}
+
 kda_status check_prefill(const kda_shape* shape, int32_t L, int32_t chunk, float* state, int64_t* pos,
                          const void* q, const void* k, const void* v, const float* alpha, const float* beta,
                          float* o, int32_t ckpt_every, const int32_t* ckpt_slots, const kda_slots* slots,
@@ -595,6 +654,59 @@ kda_status kda_mixed_step(const kda_shape* shape, const int32_t* roles, const in
     log->pending_form = 0;
   }
   return KDA_OK;
+}
+
+kda_status kda_kv_append(const kda_kv_shape* shape, const kda_pages* pages, const int32_t* table, int32_t max_pages,
+                         const int32_t* tok_start, int32_t n_tokens, const int64_t* pos, const void* k,
+                         int64_t k_stride, const void* v, int64_t v_stride, const void* q, int64_t q_stride,
+                         void* q_out, int64_t q_out_stride, const kda_rotation* rot, int32_t* dev_err, void* stream) {
+  kda::KvBatch b;
+  kda_status r = check_kv(shape, pages, table, max_pages, tok_start, n_tokens, pos, dev_err, &b);
+  if (r != KDA_OK) return r;
+  const kda_kv_shape& s = *shape;
+  const bool latent = is_latent(s);
+  if (rot) {
+    if (rot->max_pos < 1 || rot->dim < 16 || rot->dim % 16 != 0 || rot->start < 0 || rot->start % 16 != 0 ||
+        (int64_t)rot->start + rot->dim > s.dk)
+      return KDA_ERR_SHAPE;
+  }
+  kda::KvRows kr{k, k_stride}, vr{v, v_stride}, qr{q, q_stride}, qo{q_out, q_out_stride};
+  if ((r = check_rows(s, s.Hkv, s.dk, &kr)) != KDA_OK || (r = check_rows(s, s.Hkv, s.dv, &vr)) != KDA_OK ||
+      (r = check_rows(s, s.Hq, s.dk, &qr)) != KDA_OK || (r = check_rows(s, s.Hq, s.dk, &qo)) != KDA_OK)
+    return r;
+  if (b.s.B == 0 || n_tokens == 0) return KDA_OK;
+  if (!k || (!latent && !v) || (q == nullptr) != (q_out == nullptr) || (q && !rot) || (rot && !rot->cos_sin))
+    return KDA_ERR_NULL;
+  if (latent && v) return KDA_ERR_SHAPE;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16)) return KDA_ERR_ALIGN;
+  if (rot && !aligned(rot->cos_sin, 16)) return KDA_ERR_ALIGN;
+  return launched(kda::launch_kv_append(b, kr, vr, qr, q_out, qo.stride, rot ? *rot : kda_rotation{},
+                                        static_cast<hipStream_t>(stream)),
+                  KDA_VARIANT_KV_APPEND);
+}
+
+kda_status kda_attn_decode(const kda_kv_shape* shape, const kda_pages* pages, const int32_t* table,
+                           int32_t max_pages, const int32_t* tok_start, int32_t n_tokens, const int64_t* pos,
+                           const void* q, int64_t q_stride, float scale, int32_t window, void* o, float* lse,
+                           void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream) {
+  kda::KvBatch b;
+  kda_status r = check_kv(shape, pages, table, max_pages, tok_start, n_tokens, pos, dev_err, &b);
+  if (r != KDA_OK) return r;
+  if (shape->T > kMaxT || window < 0 || !isfinite(scale)) return KDA_ERR_SHAPE;
+  kda::KvRows qr{q, q_stride};
+  if ((r = check_rows(*shape, shape->Hq, shape->dk, &qr)) != KDA_OK) return r;
+  if (b.s.B == 0 || n_tokens == 0) return KDA_OK;
+  const size_t need = kda_attn_workspace_bytes(shape, pages, max_pages);
+  if (!q || !o || (need > 0 && !workspace)) return KDA_ERR_NULL;
+  if (workspace_bytes < need) return KDA_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256)) return KDA_ERR_ALIGN;
+  return launched(kda::launch_attn_decode(b, qr, scale, window, o, lse, workspace, static_cast<hipStream_t>(stream)),
+                  KDA_VARIANT_ATTN_DECODE);
+}
+
+size_t kda_attn_workspace_bytes(const kda_kv_shape* shape, const kda_pages* pages, int32_t max_pages) {
+  if (check_kv_shape(shape, pages, max_pages) != KDA_OK || shape->T > kMaxT) return 0;
+  return kda::attn_workspace_bytes(*shape, pages->page_size, max_pages);
 }
 
 const char* kda_status_str(kda_status status) {

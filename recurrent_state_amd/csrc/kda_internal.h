@@ -112,6 +112,30 @@ hipError_t launch_mixed(const kda_shape& s, const MixedBatch& m, float* state, i
                         int32_t n_slots, TokenInputs in, float* o, const LogPtrs* log, int32_t T_pend,
                         const int32_t* accepted, int32_t* dev_err, hipStream_t st);
 
+// Where the new tokens of a paged attention call are, and the pages they
+// reach: packed rows (tok_start) or T rows to each sequence (tok_start null).
+struct KvBatch {
+  kda_kv_shape s;
+  kda_pages pages;
+  const int32_t* table;
+  int32_t max_pages;
+  int32_t page_shift;  // log2(page_size)
+  const int32_t* tok_start;
+  int32_t n_tokens;
+  const int64_t* pos;
+  int32_t* dev_err;
+};
+struct KvRows {  // token rows `stride` elements apart
+  const void* p;
+  int64_t stride;
+};
+// rot.cos_sin null: keys are stored as they are.  q.p null: no queries.
+hipError_t launch_kv_append(const KvBatch& b, KvRows k, KvRows v, KvRows q, void* q_out, int64_t q_out_stride,
+                            const kda_rotation& rot, hipStream_t st);
+hipError_t launch_attn_decode(const KvBatch& b, KvRows q, float scale, int32_t window, void* o, float* lse,
+                              void* workspace, hipStream_t st);
+size_t attn_workspace_bytes(const kda_kv_shape& s, int32_t page_size, int32_t max_pages);
+
 // Copies whole per-sequence states (n_floats each) and positions for up to
 // kMaxPairs (src, dst) index pairs per launch.
 constexpr int kMaxPairs = 64;

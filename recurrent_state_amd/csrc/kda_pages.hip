@@ -1,0 +1,229 @@
+// Appending to the paged attention cache: new keys are rotated by their
+// positions and stored in their pages with the values, and the queries of the
+// same tokens are rotated, in one launch.
+//
+// A thread takes one unit of 16 values of one head row: two chunks of 8 that
+// hold both members of 8 rotation pairs (chunks `dim / 2` apart for pairs
+// (n, dim / 2 + n), neighbours for (2n, 2n + 1) and for values that are not
+// rotated), so nothing is exchanged between lanes and q_out may be q itself.
+// A token's units are numbered queries, keys, values; consecutive threads take
+// consecutive units, so a wave covers whole 128-byte lines of a head row.
+
+#include "kda_pages.h"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct AppendArgs {
+  KvBatch kb;
+  KvRows k, v, q;
+  void* q_out;
+  int64_t q_out_stride;
+  kda_rotation rot;
+  int32_t units_q, units_k, units;  // units of a token: queries; and keys; and values
+};
+
+// 8 values as fp32.
+__device__ __forceinline__ void load8(const bf16_t* p, float (&x)[8]) {
+  Raw<bf16_t, 8> r;
+  load_raw(p, r);
+  widen(r, x);
+}
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  Raw<float, 8> r;
+  load_raw(p, r);
+  widen(r, x);
+}
+
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(2))) float f32x2;
+
+__device__ __forceinline__ void store8(bf16_t* p, const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x[2 * i], x[2 * i + 1]}, bf16x2));
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// e4m3 of x / scale: clamped to the type's largest value (it has no infinity),
+// rounded to nearest even by the conversion.  The division is the IEEE one, so
+// the stored bits are those of the formula.
+__device__ __forceinline__ float to_range(float x, float scale) {
+  const float y = x / scale;
+  return y != y ? y : fminf(fmaxf(y, -448.f), 448.f);
+}
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&x)[8], float scale) {
+  int w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(to_range(x[4 * i], scale), to_range(x[4 * i + 1], scale), w[i], false);
+    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(to_range(x[4 * i + 2], scale), to_range(x[4 * i + 3], scale), w[i], true);
+  }
+  *reinterpret_cast<int2*>(p) = make_int2(w[0], w[1]);
+}
+
+// The sequence of packed row `row`: the last one that starts at or before it.
+// The wave finds its first row's sequence by counting starts, 64 at a time;
+// the lanes go on from there (a wave spans few rows).
+__device__ __forceinline__ int seq_of_row(const KvBatch& kb, int row) {
+  const int lane = threadIdx.x & 63;
+  const int first = __builtin_amdgcn_readfirstlane(row);
+  int b = -1;
+  for (int c = 0; c < kb.s.B; c += kWave) {
+    const bool before = c + lane < kb.s.B && kb.tok_start[c + lane] <= first;
+    const int n = __popcll(__ballot(before));
+    b += n;
+    if (n < kWave) break;
+  }
+  if (b < 0) return -1;
+  while (b + 1 < kb.s.B && kb.tok_start[b + 1] <= row) ++b;
+  return b;
+}
+
+template <int DK, int DV, typename TIn, typename TC>
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
+  constexpr bool kE4m3 = sizeof(TC) == 1;
+  const KvBatch& kb = a.kb;
+  // Ranges that do not fit the launch are named by the first block, whether
+  // or not they hold a row.
+  if (blockIdx.x == 0 && kb.tok_start)
+    for (int b = threadIdx.x; b < kb.s.B; b += kThreads)
+      if (seq_rows(kb, b).bad) set_err(kb.dev_err, KDA_DEV_ERR_TOKENS);
+
+  const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t total = (int64_t)kb.n_tokens * a.units;
+  const bool live = e < total;  // the whole wave takes part in seq_of_row
+  const int row = (int)((live ? e : total - 1) / a.units);
+  int u = (int)(e - (int64_t)row * a.units);
+  const int b = kb.tok_start ? seq_of_row(kb, row) : row / kb.s.T;
+  if (!live || b < 0) return;
+  const SeqRows sr = seq_rows(kb, b);
+  const int i = row - sr.row0;
+  if (sr.bad || i < 0 || i >= sr.n) return;
+
+  const int64_t p = kb.pos[b] + i;
+  const bool rotates = a.rot.cos_sin != nullptr;
+  if (p < 0 || (rotates && p >= a.rot.max_pos)) {
+    if (u == 0) set_err(kb.dev_err, KDA_DEV_ERR_POS);
+    return;
+  }
+  const int64_t at = p >> kb.page_shift;
+  const int32_t page = at < kb.max_pages ? kb.table[(int64_t)b * kb.max_pages + at] : -1;
+  if (page < 0 || page >= kb.pages.n_pages) {
+    if (u == 0) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
+    return;
+  }
+  const int slot = (int)p & (kb.pages.page_size - 1);
+
+  if (u >= a.units_k) {  // a value: stored as it is
+    u -= a.units_k;
+    const int h = u / (DV / 16), c = u % (DV / 16) * 16;
+    const TIn* src = static_cast<const TIn*>(a.v.p) + row * a.v.stride + h * DV + c;
+    TC* dst = static_cast<TC*>(kb.pages.v) +
+              ((((int64_t)page * kb.s.Hkv + h) << kb.page_shift) + slot) * DV + c;
+    float x[8], y[8];
+    load8(src, x);
+    load8(src + 8, y);
+    if constexpr (kE4m3) {
+      store8_e4m3(dst, x, kb.pages.v_scale[h]);
+      store8_e4m3(dst + 8, y, kb.pages.v_scale[h]);
+    } else {
+      store8(dst, x);
+      store8(dst + 8, y);
+    }
+    return;
+  }
+
+  const bool is_key = u >= a.units_q;
+  if (is_key) u -= a.units_q;
+  const int h = u / (DK / 16);
+  const int w = u % (DK / 16);
+  // The unit's two chunks: rotated units come first.
+  const int n_rot = rotates ? a.rot.dim >> 4 : 0;
+  const bool turn = w < n_rot;
+  int c0, c1;
+  if (turn) {
+    c0 = a.rot.start + (a.rot.pairs ? 16 * w : 8 * w);
+    c1 = c0 + (a.rot.pairs ? 8 : a.rot.dim >> 1);
+  } else {
+    c0 = 16 * (w - n_rot);
+    if (rotates && c0 >= a.rot.start) c0 += a.rot.dim;
+    c1 = c0 + 8;
+  }
+  const TIn* src = is_key ? static_cast<const TIn*>(a.k.p) + row * a.k.stride + h * DK
+                          : static_cast<const TIn*>(a.q.p) + row * a.q.stride + h * DK;
+  float x[8], y[8];
+  load8(src + c0, x);
+  load8(src + c1, y);
+  if (turn) {
+    const float* cs = a.rot.cos_sin + p * a.rot.dim + 8 * w;
+    float cc[8], ss[8];
+    load8(cs, cc);
+    load8(cs + (a.rot.dim >> 1), ss);
+    if (a.rot.pairs) {
+      // x holds pairs 0..3 interleaved, y pairs 4..7.
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float x0 = x[2 * n], x1 = x[2 * n + 1], y0 = y[2 * n], y1 = y[2 * n + 1];
+        x[2 * n] = x0 * cc[n] - x1 * ss[n];
+        x[2 * n + 1] = x1 * cc[n] + x0 * ss[n];
+        y[2 * n] = y0 * cc[4 + n] - y1 * ss[4 + n];
+        y[2 * n + 1] = y1 * cc[4 + n] + y0 * ss[4 + n];
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const float x0 = x[n], y0 = y[n];
+        x[n] = x0 * cc[n] - y0 * ss[n];
+        y[n] = y0 * cc[n] + x0 * ss[n];
+      }
+    }
+  }
+  if (!is_key) {
+    TIn* dst = static_cast<TIn*>(a.q_out) + row * a.q_out_stride + h * DK;
+    store8(dst + c0, x);
+    store8(dst + c1, y);
+    return;
+  }
+  TC* dst = static_cast<TC*>(kb.pages.k) + ((((int64_t)page * kb.s.Hkv + h) << kb.page_shift) + slot) * DK;
+  if constexpr (kE4m3) {
+    store8_e4m3(dst + c0, x, kb.pages.k_scale[h]);
+    store8_e4m3(dst + c1, y, kb.pages.k_scale[h]);
+  } else {
+    store8(dst + c0, x);
+    store8(dst + c1, y);
+  }
+}
+
+template <int DK, int DV, typename TIn, typename TC>
+hipError_t run(const AppendArgs& a, hipStream_t st) {
+  const int64_t blocks = ((int64_t)a.kb.n_tokens * a.units + kThreads - 1) / kThreads;
+  hipLaunchKernelGGL((append_kernel<DK, DV, TIn, TC>), dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const KvBatch& b, KvRows k, KvRows v, KvRows q, void* q_out, int64_t q_out_stride,
+                            const kda_rotation& rot, hipStream_t st) {
+  AppendArgs a{b, k, v, q, q_out, q_out_stride, rot, 0, 0, 0};
+  a.units_q = q.p ? b.s.Hq * (b.s.dk / 16) : 0;
+  a.units_k = a.units_q + b.s.Hkv * (b.s.dk / 16);
+  a.units = a.units_k + (v.p ? b.s.Hkv * (b.s.dv / 16) : 0);
+  if (b.s.dk == 576) return run<576, 512, bf16_t, bf16_t>(a, st);
+  const bool wide = b.s.dk == 128;
+  if (b.s.in_dtype == KDA_F32)
+    return wide ? run<128, 128, float, float>(a, st) : run<64, 64, float, float>(a, st);
+  if (b.s.cache_dtype == KDA_E4M3)
+    return wide ? run<128, 128, bf16_t, uint8_t>(a, st) : run<64, 64, bf16_t, uint8_t>(a, st);
+  return wide ? run<128, 128, bf16_t, bf16_t>(a, st) : run<64, 64, bf16_t, bf16_t>(a, st);
+}
+
+}  // namespace kda
