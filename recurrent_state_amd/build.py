@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkda.so")
 
 SOURCES = ["kda_api.cpp", "kda_state.hip", "kda_verify.hip", "kda_slots.hip", "kda_prefill.hip", "kda_mixed.hip",
-           "kda_pages.hip", "kda_attn.hip"]
+           "kda_pages.hip", "kda_attn.hip", "kda_attn_latent.hip"]
 
 # -ffp-contract=off: every fused multiply-add in the kernels is written out,
 #   so decode and commit round identically.

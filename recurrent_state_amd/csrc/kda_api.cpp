@@ -154,6 +154,7 @@ kda_status check_kv(const kda_kv_shape* s, const kda_pages* pages, const int32_t
   if ((int64_t)n_tokens * units > (int64_t)1 << 38) return KDA_ERR_SHAPE;
   if (s->B > 0 && n_tokens > 0) {
     const bool latent = is_latent(*s);
+    if (pages->n_pages < 1) return KDA_ERR_SHAPE;
     if (!table || !pos || !dev_err || !pages->k || (!latent && !pages->v)) return KDA_ERR_NULL;
     if (latent && pages->v) return KDA_ERR_SHAPE;
     if (s->cache_dtype == KDA_E4M3 && (!pages->k_scale || !pages->v_scale)) return KDA_ERR_NULL;

@@ -1,102 +1,656 @@
-// Attention of a sequence's new tokens over its paged cache.
+// Attention of a sequence's new tokens over its paged cache, heads grouped.
 //
-// One wave per query row and head walks the tokens that the row sees, with the
-// softmax's running maximum and sum: m' = max(m, s), l = l e^(m - m') +
-// e^(s - m'), and the output the same.  Everything after the loads is fp32.
+// A workgroup of four waves takes a run of tiles (kda_attn_impl.h) of one kv
+// head; each wave a quarter of every tile.  The T new tokens' G = Hq / Hkv
+// query heads that share the kv head are the rows of one matrix, 16 to an
+// MFMA tile, so a cached row is read once for all of them.  The work is bound
+// by that read, and everything else stays out of its way: keys and values go
+// from memory straight into the registers of the matrix instructions, without
+// LDS, barriers or exchanges between lanes.
+//
+//   S^T = K Q^T    keys are the first operand: lane l holds key l & 15 of 16,
+//                  the 16 bytes that its k-slot group l >> 4 needs.
+//   softmax        S^T leaves the MFMA with a query row to each lane column
+//                  and tokens 4 (l >> 4) + i in its registers: the row maximum
+//                  is a maximum over registers and two lane swaps.
+//   O^T = V^T P^T  P^T is used where it is.  The contraction index may be
+//                  permuted as long as both operands agree: k-slot (g, e)
+//                  stands for token 4 g + e (e < 4) or 16 + 4 g + e - 4, which
+//                  is the token whose probability the lane already holds.  V^T
+//                  is formed from eight row loads by byte permutations: lane l
+//                  loads 8 (or 4) neighbouring values of its group's tokens,
+//                  and V^T tile c takes the c-th of each.
+//   epilogue       O^T has dv / 4 neighbouring outputs of one row in a lane.
+//
+// fp32 caches take the same paths through v_mfma_f32_16x16x4_f32 (no
+// permutations: an operand is one value per lane); e4m3 values are widened to
+// bf16, which holds each of them exactly, and their scales enter the softmax
+// scale and the result.
+//
+// Rounding: scores, maxima, sums and outputs are fp32; for bf16 queries the
+// probabilities are rounded to bf16 (relative 2^-8, in the order of the
+// result's own rounding) because the matrix instruction takes them so.
 
-#include "kda_pages.h"
+#include <type_traits>
+
+#include "kda_attn_impl.h"
 
 namespace kda {
 namespace {
 
-struct AttnArgs {
-  KvBatch kb;
-  KvRows q;
-  float scale;
-  int32_t window;
-  void* o;
-  float* lse;
-};
+constexpr int kWaves = 4;
 
-__device__ __forceinline__ float widen1(bf16_t x) { return __uint_as_float((uint32_t)x << 16); }
-__device__ __forceinline__ float widen1(float x) { return x; }
-__device__ __forceinline__ float widen1(uint8_t x) { return __builtin_amdgcn_cvt_f32_fp8((int)x, 0); }
-__device__ __forceinline__ void store1(bf16_t* p, float x) { *p = __builtin_bit_cast(uint16_t, (__bf16)x); }
-__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
+typedef __attribute__((ext_vector_type(2))) uint16_t u16x2;
 
-template <int DK, int DV, typename TIn, typename TC>
-__global__ void __launch_bounds__(kWave) attn_kernel(AttnArgs a) {
-  constexpr bool kLatent = DK != DV;
-  const KvBatch& kb = a.kb;
-  const int lane = threadIdx.x, b = blockIdx.x / kb.s.T, i = blockIdx.x % kb.s.T, h = blockIdx.y;
-  const int hk = h / (kb.s.Hq / kb.s.Hkv);
-  const SeqRows sr = seq_rows(kb, b);
-  if (sr.bad && lane == 0) set_err(kb.dev_err, KDA_DEV_ERR_TOKENS);
-  if (sr.bad || i >= sr.n) return;
-  const int64_t pos = kb.pos[b], p = pos + i, end = pos + sr.n;
-  const int32_t* table = kb.table + (int64_t)b * kb.max_pages;
-  bool bad = end > ((int64_t)kb.max_pages << kb.page_shift);
-  if (!bad && end > 0) {
-    const int64_t lo = a.window > 0 && pos + 1 > a.window ? pos + 1 - a.window : 0;
-    for (int64_t g = (lo >> kb.page_shift) + lane; g <= (end - 1) >> kb.page_shift; g += kWave)
-      bad |= table[g] < 0 || table[g] >= kb.pages.n_pages;
-  }
-  if (__ballot(bad) != 0) {
-    if (lane == 0) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
-    return;
-  }
-  const int row = sr.row0 + i;
-  const TIn* q = static_cast<const TIn*>(a.q.p) + row * a.q.stride + h * DK;
-  float qv[DK / kWave], acc[DV / kWave], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int d = 0; d < DK / kWave; ++d) qv[d] = widen1(q[d * kWave + lane]);
-#pragma unroll
-  for (int d = 0; d < DV / kWave; ++d) acc[d] = 0.f;
-  const float ks = kb.pages.k_scale ? kb.pages.k_scale[hk] : 1.f;
-  const float vs = kb.pages.v_scale && !kLatent ? kb.pages.v_scale[hk] : 1.f;
-  for (int64_t j = a.window > 0 && p + 1 > a.window ? p + 1 - a.window : 0; j <= p; ++j) {
-    const int64_t at = (((int64_t)table[j >> kb.page_shift] * kb.s.Hkv + hk) << kb.page_shift) +
-                       (j & (kb.pages.page_size - 1));
-    const TC* k = static_cast<const TC*>(kb.pages.k) + at * DK;
-    const TC* v = kLatent ? k : static_cast<const TC*>(kb.pages.v) + at * DV;
-    float s = 0.f;
-#pragma unroll
-    for (int d = 0; d < DK / kWave; ++d) s = __builtin_fmaf(qv[d], widen1(k[d * kWave + lane]), s);
-    s = wave_sum(s) * ks * a.scale;
-    const float mn = fmaxf(m, s), keep = m == mn ? 1.f : __expf(m - mn);
-    const float w = s == -INFINITY ? 0.f : __expf(s - mn);
-    m = mn;
-    l = l * keep + w;
-#pragma unroll
-    for (int d = 0; d < DV / kWave; ++d) acc[d] = acc[d] * keep + w * widen1(v[d * kWave + lane]);
-  }
-  const float inv = l == 0.f ? 0.f : vs / l;
-  TIn* o = static_cast<TIn*>(a.o) + ((int64_t)row * kb.s.Hq + h) * DV;
-#pragma unroll
-  for (int d = 0; d < DV / kWave; ++d) store1(o + d * kWave + lane, acc[d] * inv);
-  if (a.lse && lane == 0) a.lse[(int64_t)row * kb.s.Hq + h] = m + __logf(l);
+__device__ __forceinline__ f32x4 mfma_bf16(const bf16x8& a, const bf16x8& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
+}
+__device__ __forceinline__ bf16x8 as_op(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_bit_cast(bf16x8, (u32x4){a, b, c, d});
+}
+__device__ __forceinline__ float widen(bf16_t x) { return __uint_as_float((uint32_t)x << 16); }
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(uint8_t x) { return __builtin_amdgcn_cvt_f32_fp8((int)x, 0); }
+// Two e4m3 values (the low or high pair of w) as packed bf16, exactly.
+template <bool HI>
+__device__ __forceinline__ uint32_t widen_e4m3(uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, HI));
 }
 
-template <int DK, int DV, typename TIn, typename TC>
+// The probabilities of 32 tokens as an operand, and products with V^T tiles:
+// w holds two neighbouring columns of the lane's eight tokens.
+template <int NQ>
+struct Weights {
+  bf16x8 p[NQ];
+
+  __device__ __forceinline__ explicit Weights(const f32x4 (&x)[NQ][2]) {
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+      p[n] = as_op(pack2(x[n][0][0], x[n][0][1]), pack2(x[n][0][2], x[n][0][3]), pack2(x[n][1][0], x[n][1][1]),
+                   pack2(x[n][1][2], x[n][1][3]));
+  }
+  template <int VC>
+  __device__ __forceinline__ void add(const uint32_t (&w)[8], bool high, f32x4 (&out)[NQ][VC], int c) const {
+    uint32_t x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], high ? 0x07060302u : 0x05040100u);
+    const bf16x8 vt = as_op(x[0], x[1], x[2], x[3]);
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) out[n][c] = mfma_bf16(vt, p[n], out[n][c]);
+  }
+};
+
+// One wave's share of the keys and values of SUB tokens, in the layout that
+// the loads give, and the operands made from it.  Token t of the share is row
+// `t & 15` of group `t >> 4`; pk / pv point to each group's first row.
+//
+// bf16: 32 tokens, 32 contraction slots.
+template <int D, typename TC>
+struct Cache;
+
+template <int D>
+struct Cache<D, bf16_t> {
+  static constexpr int GROUPS = 2, SUB = 32;
+  static constexpr int VC = D / 16;  // neighbouring values of a row in a lane
+  u32x4 k[2][D / 32];
+  uint32_t v[8][VC / 2];
+  struct Query {
+    bf16x8 q[D / 32];
+  };
+
+  static __device__ __forceinline__ void load_query(Query& q, const bf16_t* row, bool live) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s)
+      q.q[s] = live ? *reinterpret_cast<const bf16x8*>(row + 32 * s + 8 * g) : bf16x8{};
+  }
+  __device__ __forceinline__ void load_k(int u, const bf16_t* rows) {
+    const int l = threadIdx.x & 63;
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s)
+      k[u][s] = *reinterpret_cast<const u32x4*>(rows + (l & 15) * D + 32 * s + 8 * (l >> 4));
+  }
+  __device__ __forceinline__ void load_v(int u, const bf16_t* rows) {
+    const int l = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bf16_t* p = rows + (4 * (l >> 4) + j) * D + VC * (l & 15);
+      if constexpr (VC == 8) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * u + j][i] = w[i];
+      } else {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+        v[4 * u + j][0] = w[0];
+        v[4 * u + j][1] = w[1];
+      }
+    }
+  }
+  __device__ __forceinline__ f32x4 score(int u, const Query& q) const {
+    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) c = mfma_bf16(__builtin_bit_cast(bf16x8, k[u][s]), q.q[s], c);
+    return c;
+  }
+  // Values of the lane's token e (of 8: group e >> 2): zero unless kept / tested.
+  __device__ __forceinline__ void keep(int e, bool kept) {
+#pragma unroll
+    for (int i = 0; i < VC / 2; ++i) v[e][i] = kept ? v[e][i] : 0;
+  }
+  // What of `acc` and token e tells a value that is not finite: the largest
+  // magnitude of the low and of the high halves.
+  __device__ __forceinline__ uint32_t peak(int e, uint32_t acc) const {
+#pragma unroll
+    for (int i = 0; i < VC / 2; ++i)
+      acc = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, acc),
+                                                                   __builtin_bit_cast(u16x2, v[e][i] & 0x7fff7fffu)));
+    return acc;
+  }
+  static __device__ __forceinline__ bool not_finite(uint32_t acc) {
+    return (acc & 0xffffu) >= 0x7f80u || acc >= 0x7f800000u;
+  }
+  // out[c] += V^T tile c times the probabilities.
+  template <int NQ>
+  __device__ __forceinline__ void weigh(const f32x4 (&p)[NQ][2], f32x4 (&out)[NQ][VC]) const {
+    const Weights<NQ> weights(p);
+#pragma unroll
+    for (int c = 0; c < VC; ++c) {
+      uint32_t w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = v[e][c / 2];
+      weights.add(w, c & 1, out, c);
+    }
+  }
+};
+
+// e4m3: as bf16, widened when used.  A key load of 16 bytes feeds two
+// contraction steps, so the queries are laid out to match.
+template <int D>
+struct Cache<D, uint8_t> {
+  static constexpr int GROUPS = 2, SUB = 32;
+  static constexpr int VC = D / 16;
+  u32x4 k[2][D / 64];
+  uint32_t v[8][VC / 4];
+  struct Query {
+    bf16x8 q[D / 32];
+  };
+
+  static __device__ __forceinline__ void load_query(Query& q, const bf16_t* row, bool live) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s)
+      q.q[s] = live ? *reinterpret_cast<const bf16x8*>(row + 64 * (s / 2) + 16 * g + 8 * (s & 1)) : bf16x8{};
+  }
+  __device__ __forceinline__ void load_k(int u, const uint8_t* rows) {
+    const int l = threadIdx.x & 63;
+#pragma unroll
+    for (int s = 0; s < D / 64; ++s)
+      k[u][s] = *reinterpret_cast<const u32x4*>(rows + (l & 15) * D + 64 * s + 16 * (l >> 4));
+  }
+  __device__ __forceinline__ void load_v(int u, const uint8_t* rows) {
+    const int l = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint8_t* p = rows + (4 * (l >> 4) + j) * D + VC * (l & 15);
+      if constexpr (VC == 8) {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+        v[4 * u + j][0] = w[0];
+        v[4 * u + j][1] = w[1];
+      } else {
+        v[4 * u + j][0] = *reinterpret_cast<const uint32_t*>(p);
+      }
+    }
+  }
+  __device__ __forceinline__ f32x4 score(int u, const Query& q) const {
+    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+      const uint32_t a = k[u][s / 2][2 * (s & 1)], b = k[u][s / 2][2 * (s & 1) + 1];
+      c = mfma_bf16(as_op(widen_e4m3<false>(a), widen_e4m3<true>(a), widen_e4m3<false>(b), widen_e4m3<true>(b)),
+                    q.q[s], c);
+    }
+    return c;
+  }
+  __device__ __forceinline__ void keep(int e, bool kept) {
+#pragma unroll
+    for (int i = 0; i < VC / 4; ++i) v[e][i] = kept ? v[e][i] : 0;
+  }
+  // The type has NaN only, all ones but the sign: adding one carries into it.
+  __device__ __forceinline__ uint32_t peak(int e, uint32_t acc) const {
+#pragma unroll
+    for (int i = 0; i < VC / 4; ++i) acc |= (v[e][i] & 0x7f7f7f7fu) + 0x01010101u;
+    return acc;
+  }
+  static __device__ __forceinline__ bool not_finite(uint32_t acc) { return (acc & 0x80808080u) != 0; }
+  template <int NQ>
+  __device__ __forceinline__ void weigh(const f32x4 (&p)[NQ][2], f32x4 (&out)[NQ][VC]) const {
+    const Weights<NQ> weights(p);
+#pragma unroll
+    for (int c = 0; c < VC; c += 2) {
+      uint32_t w[8];  // columns c and c + 1 of the lane's tokens
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = c & 2 ? widen_e4m3<true>(v[e][c / 4]) : widen_e4m3<false>(v[e][c / 4]);
+      weights.add(w, false, out, c);
+      weights.add(w, true, out, c + 1);
+    }
+  }
+};
+
+// fp32: 16 tokens; a contraction step takes four k-slots, one to each lane
+// group.  V^T tile (64 h + c): columns 64 h + 4 m + c.
+template <int D>
+struct Cache<D, float> {
+  static constexpr int GROUPS = 1, SUB = 16;
+  static constexpr int VC = D / 16;
+  f32x4 k[1][D / 16];
+  f32x4 v[4][D / 64];
+  struct Query {
+    f32x4 q[D / 16];
+  };
+
+  static __device__ __forceinline__ void load_query(Query& q, const float* row, bool live) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+      q.q[s] = live ? *reinterpret_cast<const f32x4*>(row + 16 * s + 4 * g) : f32x4{};
+  }
+  __device__ __forceinline__ void load_k(int u, const float* rows) {
+    const int l = threadIdx.x & 63;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+      k[u][s] = *reinterpret_cast<const f32x4*>(rows + (l & 15) * D + 16 * s + 4 * (l >> 4));
+  }
+  __device__ __forceinline__ void load_v(int, const float* rows) {
+    const int l = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+        v[j][h] = *reinterpret_cast<const f32x4*>(rows + (4 * (l >> 4) + j) * D + 64 * h + 4 * (l & 15));
+  }
+  __device__ __forceinline__ f32x4 score(int u, const Query& q) const {
+    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(k[u][s][i], q.q[s][i], c, 0, 0, 0);
+    return c;
+  }
+  __device__ __forceinline__ void keep(int e, bool kept) {
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[e][h][i] = kept ? v[e][h][i] : 0.f;
+  }
+  __device__ __forceinline__ uint32_t peak(int e, uint32_t acc) const {
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc = max(acc, __float_as_uint(v[e][h][i]) & 0x7fffffffu);
+    return acc;
+  }
+  static __device__ __forceinline__ bool not_finite(uint32_t acc) { return acc >= 0x7f800000u; }
+  template <int NQ>
+  __device__ __forceinline__ void weigh(const f32x4 (&p)[NQ][1], f32x4 (&out)[NQ][VC]) const {
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+            out[n][4 * h + c] =
+                __builtin_amdgcn_mfma_f32_16x16x4f32(v[j][h][c], p[n][0][j], out[n][4 * h + c], 0, 0, 0);
+  }
+};
+
+// Column of the output that register i of tile c holds in lane group g.
+template <int D, typename TC>
+__device__ __forceinline__ int out_col(int g, int c, int i) {
+  if constexpr (sizeof(TC) == 4) return 64 * (c / 4) + 4 * (4 * g + i) + c % 4;
+  return D / 16 * (4 * g + i) + c;
+}
+
+__device__ __forceinline__ void store8(bf16_t* p, const float (&x)[8]) {
+  *reinterpret_cast<u32x4*>(p) =
+      (u32x4){pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])};
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<f32x4*>(p)[0] = (f32x4){x[0], x[1], x[2], x[3]};
+  reinterpret_cast<f32x4*>(p)[1] = (f32x4){x[4], x[5], x[6], x[7]};
+}
+
+// NQ blocks of 16 query rows to a workgroup.
+template <int D, typename TIn, typename TC, int NQ>
+__global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1) attn_kernel(AttnArgs a) {
+  typedef Cache<D, TC> C;
+  constexpr int SUB = C::SUB, GROUPS = C::GROUPS, VC = C::VC, TILE = kWaves * SUB;
+  constexpr int RS = D + 4;  // LDS row stride in floats
+  __shared__ float lds_o[kWaves][16][RS];
+  __shared__ f32x2 lds_ml[kWaves][16];
+
+  const KvBatch& kb = a.kb;
+  const int wave = uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int hk = blockIdx.y, rb = blockIdx.z, worker = blockIdx.x;
+  const int G = kb.s.Hq / kb.s.Hkv;
+  const Run run = find_run<TILE>(a, worker, worker == 0 && hk == 0 && rb == 0 && wave == 0);
+  float x_scale = a.scale * kLog2e;
+  if (sizeof(TC) == 1) x_scale *= kb.pages.k_scale[hk];
+  const float v_scale = sizeof(TC) == 1 ? kb.pages.v_scale[hk] : 1.f;
+
+  int64_t tile = run.tile, first = run.first;
+  for (int b = run.b; tile < run.end && b < kb.s.B; ++b) {
+    const Seq s = uniform_seq<TILE>(a, b);
+    if (s.tiles == 0) continue;
+    const int64_t stop = min(run.end, first + s.tiles);
+    const int R = s.n * G;
+    if (rb * 16 * NQ < R) {
+      // Queries, and the last visible token of the lane's row in each block.
+      typename C::Query q[NQ];
+      int vis[NQ];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        const int r = (rb * NQ + n) * 16 + (here(lane) & 15), t = r / G;
+        const bool live = r < R;
+        vis[n] = live ? (int)max(s.pos + t, (int64_t)-1) : -1;
+        C::load_query(q[n], static_cast<const TIn*>(a.q.p) + (int64_t)(s.row0 + t) * a.q.stride +
+                                (hk * G + r % G) * D, live);
+      }
+      f32x4 out[NQ][VC];
+      float m[NQ], l[NQ];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        m[n] = -INFINITY;
+        l[n] = 0.f;
+#pragma unroll
+        for (int c = 0; c < VC; ++c) out[n][c] = f32x4{};
+      }
+
+      // This wave's tokens: t0, t0 + TILE, ... below `past`.
+      const int base = (s.lo & ~(TILE - 1)) + wave * SUB;
+      int t0 = base + (int)(tile - first) * TILE;
+      const int past = min(s.end, base - wave * SUB + (int)(stop - first) * TILE);
+      // Tokens below all_lo or past the first row's are hidden from some row.
+      const int all_lo = a.window > 0 ? max((int)(s.pos + s.n) - a.window, 0) : 0;
+      C cache;
+      PageWalk walk(kb, s, b, hk);
+      const TC* const pages_k = static_cast<const TC*>(kb.pages.k);
+      const TC* const pages_v = static_cast<const TC*>(kb.pages.v);
+      int32_t id[GROUPS];  // page entries of the tile to be loaded next
+      int64_t at[GROUPS];
+      auto load_k = [&](int token) {
+#pragma unroll
+        for (int u = 0; u < GROUPS; ++u) {
+          at[u] = walk.row(token + 16 * u, id[u]);
+          cache.load_k(u, pages_k + at[u] * D);
+          id[u] = walk.entry(token + TILE + 16 * u);
+        }
+      };
+      auto load_v = [&] {
+#pragma unroll
+        for (int u = 0; u < GROUPS; ++u) cache.load_v(u, pages_v + at[u] * D);
+      };
+      f32x4 p[NQ][GROUPS];
+      auto scores = [&] {
+#pragma unroll
+        for (int u = 0; u < GROUPS; ++u)
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) p[n][u] = cache.score(u, q[n]);
+      };
+      // Scores to probabilities, and the earlier sums to the new maximum.
+      // PART: some row does not see some token.
+      auto softmax = [&](auto part) {
+        constexpr bool PART = decltype(part)::value;
+        const int g = PART ? here(lane) >> 4 : 0;
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          const int low = a.window > 0 ? vis[n] - a.window : -1;
+          float top = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < GROUPS; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float x = p[n][u][i] * x_scale;
+              const int j = t0 + 16 * u + 4 * g + i;
+              if (PART && (j > vis[n] || j <= low)) x = -INFINITY;
+              p[n][u][i] = x;
+              top = fmaxf(top, x);
+            }
+          const float mn = fmaxf(m[n], max_over_rows(top));
+          const float mu = mn == -INFINITY ? 0.f : mn, keep = exp2_(m[n] - mu);
+          m[n] = mn;
+          float sum = 0.f;
+#pragma unroll
+          for (int u = 0; u < GROUPS; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              p[n][u][i] = exp2_(p[n][u][i] - mu);
+              sum += p[n][u][i];
+            }
+          l[n] = l[n] * keep + sum;
+#pragma unroll
+          for (int c = 0; c < VC; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[n][c][i] *= keep;
+        }
+      };
+      if (t0 < past) {
+#pragma unroll
+        for (int u = 0; u < GROUPS; ++u) id[u] = walk.entry(t0 + 16 * u);
+      }
+      while (t0 < past) {
+        load_k(t0);
+        load_v();
+        // Tiles that every row sees whole, but the last: the next keys are
+        // asked for before the softmax, the next values after the products.
+        for (; t0 >= all_lo && t0 + SUB - 1 <= s.pos && t0 + TILE < past; t0 += TILE) {
+          scores();
+          load_k(t0 + TILE);
+          softmax(std::false_type{});
+          cache.weigh(p, out);
+          load_v();
+        }
+        scores();
+        softmax(std::true_type{});
+        // A probability of zero must meet a finite value.  Tokens that no row
+        // sees count as zeros; where one that only some rows see is not finite,
+        // the tokens of that kind are left to the loop below.
+        const int g = here(lane) >> 4;
+        uint32_t odd = 0;
+#pragma unroll
+        for (int e = 0; e < 4 * GROUPS; ++e) {
+          const int j = t0 + 16 * (e >> 2) + 4 * g + (e & 3);
+          cache.keep(e, (j >= s.lo) & (j < s.end));
+          const uint32_t with = cache.peak(e, odd);
+          odd = j < all_lo || j > s.pos ? with : odd;
+        }
+        if (__ballot(C::not_finite(odd)) != 0) {
+#pragma unroll
+          for (int e = 0; e < 4 * GROUPS; ++e) {
+            const int j = t0 + 16 * (e >> 2) + 4 * g + (e & 3);
+            cache.keep(e, (j >= all_lo) & (j <= s.pos));
+          }
+          // Token by token, each for the rows that see it: the probabilities
+          // go through this wave's part of the LDS, [token][row].
+          float* const plane = &lds_o[wave][0][0];
+          const int col = here(lane) & 15;
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int e = 0; e < 4 * GROUPS; ++e)
+              plane[(16 * (e >> 2) + 4 * g + (e & 3)) * 16 + col] = p[n][e >> 2][e & 3];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            for (int j = max(t0, s.lo); j < min(t0 + SUB, s.end); ++j) {
+              if (j >= all_lo && j <= s.pos) continue;
+              const float w = plane[(j - t0) * 16 + col];
+              const bool sees = j <= vis[n] && (a.window == 0 || j > vis[n] - a.window);
+              const TC* const v = pages_v + (walk.row(j & ~15, walk.entry(j)) + (j & 15)) * D;
+#pragma unroll
+              for (int c = 0; c < VC; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float x = out[n][c][i] + w * widen(v[out_col<D, TC>(g, c, i)]);
+                  out[n][c][i] = sees ? x : out[n][c][i];
+                }
+            }
+          }
+        }
+        cache.weigh(p, out);
+        t0 += TILE;
+      }
+
+      // The waves' results meet in LDS, 16 rows at a time.
+      const int tid = here((int)threadIdx.x), col = tid & 15, g = (tid & 63) >> 4;
+      const bool complete = tile == first && stop == first + s.tiles;
+      const int64_t piece = piece_index(a, worker, tile > first ? 0 : 1, hk, rb);
+      const bool bad = __syncthreads_or(walk.bad);
+      if (tid == 0) {
+        if (bad) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
+        if (!complete) a.piece_bad[piece] = bad;
+      }
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        float total = l[n];
+        total = pair_sum32(pair_sum16(total));
+        if (g == 0) lds_ml[wave][col] = (f32x2){m[n], total};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < VC; c += 4)
+            *reinterpret_cast<f32x4*>(&lds_o[wave][col][out_col<D, TC>(g, c, i)]) =
+                (f32x4){out[n][c][i], out[n][c + 1][i], out[n][c + 2][i], out[n][c + 3][i]};
+        __syncthreads();
+        constexpr int PER = D / 8;  // threads to a row
+        for (int x = tid; x < 16 * PER; x += kWaves * kWave) {
+          const int in = x / PER, c0 = x % PER * 8, r = (rb * NQ + n) * 16 + in;
+          float M = -INFINITY, L = 0.f, o[8] = {};
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) M = fmaxf(M, lds_ml[w][in][0]);
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) {
+            const f32x2 ml = lds_ml[w][in];
+            const float f = ml[0] == -INFINITY ? 0.f : exp2_(ml[0] - M);
+            L += ml[1] * f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] += lds_o[w][in][c0 + i] * f;
+          }
+          if (r < R) {
+            if (!complete) {
+              const int64_t row = piece * a.rows + 16 * n + in;
+              store8(a.piece_o + row * D + c0, o);
+              if (c0 == 0) a.piece_ml[row] = (f32x2){M, L};
+            } else if (!bad) {
+              const float inv = L == 0.f ? 0.f : v_scale / L;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] *= inv;
+              const int64_t row = (int64_t)(s.row0 + r / G) * kb.s.Hq + hk * G + r % G;
+              store8(static_cast<TIn*>(a.o) + row * D + c0, o);
+              if (a.lse && c0 == 0) a.lse[row] = (M + __log2f(L)) * kLn2;
+            }
+          }
+        }
+        __syncthreads();
+      }
+    }
+    first += s.tiles;
+    tile = stop;
+  }
+}
+
+// Blocks of 16 query rows that a workgroup takes: all of them up to four (two
+// in fp32, whose operands need twice the registers), so that a cached row is
+// read once; more rows make more workgroups.
+int query_blocks(const kda_kv_shape& s) {
+  const int rows = s.T * (s.Hq / s.Hkv);
+  if (rows <= 16) return 1;
+  return rows <= 32 || s.in_dtype == KDA_F32 ? 2 : 4;
+}
+
+struct Split {
+  int tile, rows, row_blocks, workers;
+};
+
+Split split_of(const kda_kv_shape& s, int32_t page_size, int32_t max_pages) {
+  const int nq = query_blocks(s);
+  Split d;
+  d.tile = kWaves * (s.in_dtype == KDA_F32 ? 16 : 32);
+  d.rows = 16 * nq;
+  d.row_blocks = (s.T * (s.Hq / s.Hkv) + d.rows - 1) / d.rows;
+  // As many workgroups as the chip holds at once (256 CUs), at most one to a
+  // tile of the longest possible cache.
+  const int64_t per_cu = nq == 1 ? 3 : nq == 2 ? 2 : 1;
+  int64_t w = 256 * per_cu / ((int64_t)s.Hkv * d.row_blocks);
+  const int64_t most = (int64_t)s.B * (((int64_t)max_pages * page_size + d.tile - 1) / d.tile + 1);
+  if (w > most) w = most;
+  d.workers = w < 1 ? 1 : (int)w;
+  return d;
+}
+
+struct Layout {
+  size_t bad, ml, o, total;
+};
+Layout layout_of(const kda_kv_shape& s, const Split& d) {
+  const size_t pieces = (size_t)d.workers * 2 * s.Hkv * d.row_blocks;
+  Layout L;
+  L.bad = round_up(((size_t)s.B + 1) * 8, 256);
+  L.ml = round_up(L.bad + pieces * 4, 256);
+  L.o = round_up(L.ml + pieces * d.rows * 8, 256);
+  L.total = round_up(L.o + pieces * d.rows * s.dv * 4, 256);
+  return L;
+}
+
+template <int D, typename TIn, typename TC, int NQ>
 hipError_t run(const AttnArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((attn_kernel<DK, DV, TIn, TC>), dim3(a.kb.s.B * a.kb.s.T, a.kb.s.Hq), dim3(kWave), 0, st, a);
+  const kda_kv_shape& s = a.kb.s;
+  hipLaunchKernelGGL((attn_kernel<D, TIn, TC, NQ>), dim3(a.workers, s.Hkv, a.row_blocks), dim3(kWaves * kWave), 0, st,
+                     a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.workers == 1) return e;
+  // Join: about 2048 workgroups at most, a row or more to each.
+  const int rows = s.T * (s.Hq / s.Hkv);
+  const int64_t wanted = ((int64_t)s.B * s.Hkv * rows + 2047) / 2048;
+  const int each = wanted < 1 ? 1 : wanted > rows ? rows : (int)wanted;
+  hipLaunchKernelGGL((join_kernel<D, TIn>), dim3(s.B, s.Hkv, (rows + each - 1) / each), dim3(kJoinThreads), 0, st, a,
+                     each);
   return hipGetLastError();
+}
+
+template <typename TIn, typename TC>
+hipError_t by_size(const AttnArgs& a, hipStream_t st) {
+  const bool wide = a.kb.s.dk == 128;
+  switch (a.rows) {
+    case 16: return wide ? run<128, TIn, TC, 1>(a, st) : run<64, TIn, TC, 1>(a, st);
+    case 32: return wide ? run<128, TIn, TC, 2>(a, st) : run<64, TIn, TC, 2>(a, st);
+  }
+  if constexpr (sizeof(TIn) == 2) return wide ? run<128, TIn, TC, 4>(a, st) : run<64, TIn, TC, 4>(a, st);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(const kda_kv_shape&, int32_t, int32_t) { return 256; }
+size_t attn_workspace_bytes(const kda_kv_shape& s, int32_t page_size, int32_t max_pages) {
+  if (s.dk == 576) return latent_workspace_bytes(s, page_size, max_pages);
+  return layout_of(s, split_of(s, page_size, max_pages)).total;
+}
 
-hipError_t launch_attn_decode(const KvBatch& b, KvRows q, float scale, int32_t window, void* o, float* lse, void*,
-                              hipStream_t st) {
-  const AttnArgs a{b, q, scale, window, o, lse};
-  if (b.s.dk == 576) return run<576, 512, bf16_t, bf16_t>(a, st);
-  const bool wide = b.s.dk == 128;
-  if (b.s.in_dtype == KDA_F32)
-    return wide ? run<128, 128, float, float>(a, st) : run<64, 64, float, float>(a, st);
-  if (b.s.cache_dtype == KDA_E4M3)
-    return wide ? run<128, 128, bf16_t, uint8_t>(a, st) : run<64, 64, bf16_t, uint8_t>(a, st);
-  return wide ? run<128, 128, bf16_t, bf16_t>(a, st) : run<64, 64, bf16_t, bf16_t>(a, st);
+hipError_t launch_attn_decode(const KvBatch& b, KvRows q, float scale, int32_t window, void* o, float* lse,
+                              void* workspace, hipStream_t st) {
+  if (b.s.dk == 576) return launch_attn_latent(b, q, scale, window, o, lse, workspace, st);
+  const Split d = split_of(b.s, b.pages.page_size, b.max_pages);
+  const Layout L = layout_of(b.s, d);
+  char* ws = static_cast<char*>(workspace);
+  const AttnArgs a{b,      q,          scale,  window, o, lse, d.workers, d.row_blocks, d.rows,
+                   reinterpret_cast<int64_t*>(ws), reinterpret_cast<int32_t*>(ws + L.bad),
+                   reinterpret_cast<f32x2*>(ws + L.ml), reinterpret_cast<float*>(ws + L.o)};
+  if (b.s.in_dtype == KDA_F32) return by_size<float, float>(a, st);
+  if (b.s.cache_dtype == KDA_E4M3) return by_size<bf16_t, uint8_t>(a, st);
+  return by_size<bf16_t, bf16_t>(a, st);
 }
 
 }  // namespace kda

@@ -135,6 +135,10 @@ hipError_t launch_kv_append(const KvBatch& b, KvRows k, KvRows v, KvRows q, void
 hipError_t launch_attn_decode(const KvBatch& b, KvRows q, float scale, int32_t window, void* o, float* lse,
                               void* workspace, hipStream_t st);
 size_t attn_workspace_bytes(const kda_kv_shape& s, int32_t page_size, int32_t max_pages);
+// Their latent form.
+hipError_t launch_attn_latent(const KvBatch& b, KvRows q, float scale, int32_t window, void* o, float* lse,
+                              void* workspace, hipStream_t st);
+size_t latent_workspace_bytes(const kda_kv_shape& s, int32_t page_size, int32_t max_pages);
 
 // Copies whole per-sequence states (n_floats each) and positions for up to
 // kMaxPairs (src, dst) index pairs per launch.
