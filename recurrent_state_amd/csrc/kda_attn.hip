@@ -42,15 +42,6 @@ constexpr int kWaves = 4;
 
 typedef __attribute__((ext_vector_type(2))) uint16_t u16x2;
 
-__device__ __forceinline__ f32x4 mfma_bf16(const bf16x8& a, const bf16x8& b, const f32x4& c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
-}
-__device__ __forceinline__ bf16x8 as_op(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return __builtin_bit_cast(bf16x8, (u32x4){a, b, c, d});
-}
 __device__ __forceinline__ float widen(bf16_t x) { return __uint_as_float((uint32_t)x << 16); }
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(uint8_t x) { return __builtin_amdgcn_cvt_f32_fp8((int)x, 0); }
@@ -316,15 +307,6 @@ __device__ __forceinline__ int out_col(int g, int c, int i) {
   return D / 16 * (4 * g + i) + c;
 }
 
-__device__ __forceinline__ void store8(bf16_t* p, const float (&x)[8]) {
-  *reinterpret_cast<u32x4*>(p) =
-      (u32x4){pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])};
-}
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  reinterpret_cast<f32x4*>(p)[0] = (f32x4){x[0], x[1], x[2], x[3]};
-  reinterpret_cast<f32x4*>(p)[1] = (f32x4){x[4], x[5], x[6], x[7]};
-}
-
 // NQ blocks of 16 query rows to a workgroup.
 template <int D, typename TIn, typename TC, int NQ>
 __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1) attn_kernel(AttnArgs a) {
@@ -572,53 +554,21 @@ int query_blocks(const kda_kv_shape& s) {
   return rows <= 32 || s.in_dtype == KDA_F32 ? 2 : 4;
 }
 
-struct Split {
-  int tile, rows, row_blocks, workers;
-};
-
 Split split_of(const kda_kv_shape& s, int32_t page_size, int32_t max_pages) {
   const int nq = query_blocks(s);
-  Split d;
-  d.tile = kWaves * (s.in_dtype == KDA_F32 ? 16 : 32);
-  d.rows = 16 * nq;
+  Split d{kWaves * (s.in_dtype == KDA_F32 ? 16 : 32), 16 * nq, 0, 0, 1};
   d.row_blocks = (s.T * (s.Hq / s.Hkv) + d.rows - 1) / d.rows;
-  // As many workgroups as the chip holds at once (256 CUs), at most one to a
-  // tile of the longest possible cache.
-  const int64_t per_cu = nq == 1 ? 3 : nq == 2 ? 2 : 1;
-  int64_t w = 256 * per_cu / ((int64_t)s.Hkv * d.row_blocks);
-  const int64_t most = (int64_t)s.B * (((int64_t)max_pages * page_size + d.tile - 1) / d.tile + 1);
-  if (w > most) w = most;
-  d.workers = w < 1 ? 1 : (int)w;
+  // As many workgroups as the chip's 256 CUs hold at once.
+  d.workers = workers_of(s, 256 * (nq == 1 ? 3 : nq == 2 ? 2 : 1), d, page_size, max_pages);
   return d;
-}
-
-struct Layout {
-  size_t bad, ml, o, total;
-};
-Layout layout_of(const kda_kv_shape& s, const Split& d) {
-  const size_t pieces = (size_t)d.workers * 2 * s.Hkv * d.row_blocks;
-  Layout L;
-  L.bad = round_up(((size_t)s.B + 1) * 8, 256);
-  L.ml = round_up(L.bad + pieces * 4, 256);
-  L.o = round_up(L.ml + pieces * d.rows * 8, 256);
-  L.total = round_up(L.o + pieces * d.rows * s.dv * 4, 256);
-  return L;
 }
 
 template <int D, typename TIn, typename TC, int NQ>
 hipError_t run(const AttnArgs& a, hipStream_t st) {
-  const kda_kv_shape& s = a.kb.s;
-  hipLaunchKernelGGL((attn_kernel<D, TIn, TC, NQ>), dim3(a.workers, s.Hkv, a.row_blocks), dim3(kWaves * kWave), 0, st,
-                     a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.workers == 1) return e;
-  // Join: about 2048 workgroups at most, a row or more to each.
-  const int rows = s.T * (s.Hq / s.Hkv);
-  const int64_t wanted = ((int64_t)s.B * s.Hkv * rows + 2047) / 2048;
-  const int each = wanted < 1 ? 1 : wanted > rows ? rows : (int)wanted;
-  hipLaunchKernelGGL((join_kernel<D, TIn>), dim3(s.B, s.Hkv, (rows + each - 1) / each), dim3(kJoinThreads), 0, st, a,
-                     each);
-  return hipGetLastError();
+  hipLaunchKernelGGL((attn_kernel<D, TIn, TC, NQ>), dim3(a.workers, a.kb.s.Hkv, a.row_blocks), dim3(kWaves * kWave), 0,
+                     st, a);
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess ? e : run_join<D, TIn>(a, st);
 }
 
 template <typename TIn, typename TC>
@@ -636,18 +586,14 @@ hipError_t by_size(const AttnArgs& a, hipStream_t st) {
 
 size_t attn_workspace_bytes(const kda_kv_shape& s, int32_t page_size, int32_t max_pages) {
   if (s.dk == 576) return latent_workspace_bytes(s, page_size, max_pages);
-  return layout_of(s, split_of(s, page_size, max_pages)).total;
+  return workspace_of(s, split_of(s, page_size, max_pages)).total;
 }
 
 hipError_t launch_attn_decode(const KvBatch& b, KvRows q, float scale, int32_t window, void* o, float* lse,
                               void* workspace, hipStream_t st) {
   if (b.s.dk == 576) return launch_attn_latent(b, q, scale, window, o, lse, workspace, st);
-  const Split d = split_of(b.s, b.pages.page_size, b.max_pages);
-  const Layout L = layout_of(b.s, d);
-  char* ws = static_cast<char*>(workspace);
-  const AttnArgs a{b,      q,          scale,  window, o, lse, d.workers, d.row_blocks, d.rows,
-                   reinterpret_cast<int64_t*>(ws), reinterpret_cast<int32_t*>(ws + L.bad),
-                   reinterpret_cast<f32x2*>(ws + L.ml), reinterpret_cast<float*>(ws + L.o)};
+  const AttnArgs a =
+      make_args(b, q, scale, window, o, lse, workspace, split_of(b.s, b.pages.page_size, b.max_pages));
   if (b.s.in_dtype == KDA_F32) return by_size<float, float>(a, st);
   if (b.s.cache_dtype == KDA_E4M3) return by_size<bf16_t, uint8_t>(a, st);
   return by_size<bf16_t, bf16_t>(a, st);

@@ -32,7 +32,8 @@ struct AttnArgs {
   int32_t window;
   void* o;
   float* lse;
-  int32_t workers;     // runs of the tile list
+  int32_t workers;     // runs of the tile list at most
+  int32_t run_tiles;   // tiles of a run at least, while there are enough
   int32_t row_blocks;  // blocks of query rows of a (sequence, kv head)
   int32_t rows;        // query rows of a block
   // Workspace: first tile of each sequence [B + 1], then for every piece
@@ -139,7 +140,8 @@ struct Run {
 
 // Workers with something to do: no run is empty.
 __device__ __forceinline__ int64_t busy_workers(const AttnArgs& a, int64_t total) {
-  return total < a.workers ? total : a.workers;
+  const int64_t most = (total + a.run_tiles - 1) / a.run_tiles;
+  return most < a.workers ? most : a.workers;
 }
 
 // Called by a whole wave.  `record`: this wave also names refused sequences
@@ -208,28 +210,40 @@ struct PageWalk {
   }
 };
 
-// Joins the pieces of the sequences that more than one worker had a part of.
-// One workgroup takes `rows_each` query rows of a (sequence, kv head); DV / 4
-// lanes hold a row, so several pieces are read at once, and the groups' sums
-// meet in LDS.  o = sum_w 2^(m_w - m) o_w / sum_w 2^(m_w - m) l_w.
-constexpr int kJoinThreads = 256;
-
-template <int DV>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
+}
+__device__ __forceinline__ bf16x8 as_op(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_bit_cast(bf16x8, (u32x4){a, b, c, d});
+}
+__device__ __forceinline__ f32x4 mfma_bf16(const bf16x8& a, const bf16x8& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
 __device__ __forceinline__ void store4(bf16_t* p, const f32x4& x) {
-  const uint32_t lo = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x[0], x[1]}, bf16x2));
-  const uint32_t hi = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x[2], x[3]}, bf16x2));
-  *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
 }
-template <int DV>
-__device__ __forceinline__ void store4(float* p, const f32x4& x) {
-  *reinterpret_cast<f32x4*>(p) = x;
+__device__ __forceinline__ void store4(float* p, const f32x4& x) { *reinterpret_cast<f32x4*>(p) = x; }
+__device__ __forceinline__ void store8(bf16_t* p, const float (&x)[8]) {
+  *reinterpret_cast<u32x4*>(p) =
+      (u32x4){pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])};
 }
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  store4(p, (f32x4){x[0], x[1], x[2], x[3]});
+  store4(p + 4, (f32x4){x[4], x[5], x[6], x[7]});
+}
+
+// Joins the pieces of the sequences that more than one worker had a part of:
+// with m the largest of the pieces' maxima,
+//   o = sum_w 2^(m_w - m) o_w / sum_w 2^(m_w - m) l_w.
+// One workgroup takes `rows_each` query rows of a (sequence, kv head).  Every
+// wave finds m and the sum by itself, a piece to a lane; then DV / 4 lanes hold
+// a row, eight groups of them read pieces at once, and their sums meet in LDS.
+constexpr int kJoinGroups = 8;
 
 template <int DV, typename TIn>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int rows_each) {
-  constexpr int LANES = DV / 4, GROUPS = kJoinThreads / LANES;
-  __shared__ f32x4 sum_o[GROUPS][LANES];
-  __shared__ f32x2 sum_ml[GROUPS];
+__global__ void __launch_bounds__(DV / 4 * kJoinGroups) join_kernel(AttnArgs a, int rows_each) {
+  constexpr int LANES = DV / 4;
+  __shared__ f32x4 part[kJoinGroups][LANES];
   const KvBatch& kb = a.kb;
   const int b = blockIdx.x, hk = blockIdx.y;
   const int64_t first = a.first_tile[b], past = a.first_tile[b + 1], total = a.first_tile[kb.s.B];
@@ -241,53 +255,109 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int rows
   if (w0 == w1) return;
   const int G = kb.s.Hq / kb.s.Hkv;
   const SeqRows sr = seq_rows(kb, b);
-  const int R = sr.n * G;
-  const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
-  const int r0 = blockIdx.z * rows_each, r1 = min(r0 + rows_each, R);
+  const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES, wl = threadIdx.x & 63;
+  const int r0 = blockIdx.z * rows_each, r1 = min(r0 + rows_each, sr.n * G);
   const float vs = kb.pages.v_scale ? kb.pages.v_scale[hk] : 1.f;
   for (int r = r0; r < r1; ++r) {
     const int rb = r / a.rows, in = r % a.rows;
     float m = -INFINITY, l = 0.f;
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    int bad = 0;
-    for (int w = w0 + group; w <= w1; w += GROUPS) {
+    bool bad = false;
+    for (int w = w0 + wl; w <= w1; w += kWave) {
       const int64_t at = piece_index(a, w, w == w0 ? 1 : 0, hk, rb);
-      bad |= a.piece_bad[at];
-      const f32x2 ml = a.piece_ml[at * a.rows + in];
-      const f32x4 x = *reinterpret_cast<const f32x4*>(a.piece_o + (at * a.rows + in) * DV + 4 * lane);
-      const float mn = fmaxf(m, ml[0]);
-      // A piece without visible tokens has m = -inf and zeros.
-      const float f = m == -INFINITY ? 0.f : exp2_(m - mn), g = ml[0] == -INFINITY ? 0.f : exp2_(ml[0] - mn);
-      l = l * f + ml[1] * g;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = o[i] * f + x[i] * g;
-      m = mn;
+      bad |= a.piece_bad[at] != 0;
+      m = fmaxf(m, a.piece_ml[at * a.rows + in][0]);
     }
-    bad = __syncthreads_or(bad);
-    if (lane == 0) sum_ml[group] = (f32x2){m, l};
-    sum_o[group][lane] = o;
+    if (__ballot(bad) != 0) return;  // refused: the whole workgroup sees it
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
+    // A piece in which the row sees no token has m = -inf and zeros.
+    const float top = m == -INFINITY ? 0.f : m;
+    for (int w = w0 + wl; w <= w1; w += kWave) {
+      const f32x2 ml = a.piece_ml[piece_index(a, w, w == w0 ? 1 : 0, hk, rb) * a.rows + in];
+      l += ml[1] * exp2_(ml[0] - top);
+    }
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) l += __shfl_xor(l, d);
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int w = w0 + group; w <= w1; w += kJoinGroups) {
+      const int64_t row = piece_index(a, w, w == w0 ? 1 : 0, hk, rb) * a.rows + in;
+      const float f = exp2_(a.piece_ml[row][0] - top);
+      const f32x4 x = *reinterpret_cast<const f32x4*>(a.piece_o + row * DV + 4 * lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] += x[i] * f;
+    }
+    part[group][lane] = o;
     __syncthreads();
-    if (!bad && group == 0) {
-      float M = -INFINITY, L = 0.f;
+    if (group == 0) {
 #pragma unroll
-      for (int g = 0; g < GROUPS; ++g) M = fmaxf(M, sum_ml[g][0]);
-      f32x4 x = {0.f, 0.f, 0.f, 0.f};
+      for (int g = 1; g < kJoinGroups; ++g)
 #pragma unroll
-      for (int g = 0; g < GROUPS; ++g) {
-        const float f = sum_ml[g][0] == -INFINITY ? 0.f : exp2_(sum_ml[g][0] - M);
-        L += sum_ml[g][1] * f;
+        for (int i = 0; i < 4; ++i) o[i] += part[g][lane][i];
+      const float inv = l == 0.f ? 0.f : vs / l;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] += sum_o[g][lane][i] * f;
-      }
-      const float inv = L == 0.f ? 0.f : vs / L;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] *= inv;
+      for (int i = 0; i < 4; ++i) o[i] *= inv;
       const int64_t row = (int64_t)(sr.row0 + r / G) * kb.s.Hq + hk * G + r % G;
-      store4<DV>(static_cast<TIn*>(a.o) + row * DV + 4 * lane, x);
-      if (a.lse && lane == 0) a.lse[row] = (M + __log2f(L)) * kLn2;
+      store4(static_cast<TIn*>(a.o) + row * DV + 4 * lane, o);
+      if (a.lse && lane == 0) a.lse[row] = (m + __log2f(l)) * kLn2;
     }
     __syncthreads();
   }
+}
+
+// How a call is split: see split_of() of each kernel.
+struct Split {
+  int tile, rows, row_blocks, workers, run_tiles;
+};
+
+// Workers for `wgs` workgroups on the chip at once: at most one to a shortest
+// run of the longest possible cache.
+inline int workers_of(const kda_kv_shape& s, int64_t wgs, const Split& d, int32_t page_size, int32_t max_pages) {
+  int64_t w = wgs / ((int64_t)s.Hkv * d.row_blocks);
+  const int64_t run = (int64_t)d.tile * d.run_tiles;
+  const int64_t most = (int64_t)s.B * (((int64_t)max_pages * page_size + run - 1) / run + 1);
+  if (w > most) w = most;
+  return w < 1 ? 1 : (int)w;
+}
+
+struct Workspace {
+  size_t bad, ml, o, total;
+};
+inline Workspace workspace_of(const kda_kv_shape& s, const Split& d) {
+  const size_t pieces = (size_t)d.workers * 2 * s.Hkv * d.row_blocks;
+  Workspace L;
+  L.bad = round_up(((size_t)s.B + 1) * 8, 256);
+  L.ml = round_up(L.bad + pieces * 4, 256);
+  L.o = round_up(L.ml + pieces * d.rows * 8, 256);
+  L.total = round_up(L.o + pieces * d.rows * s.dv * 4, 256);
+  return L;
+}
+
+inline AttnArgs make_args(const KvBatch& b, KvRows q, float scale, int32_t window, void* o, float* lse,
+                          void* workspace, const Split& d) {
+  const Workspace L = workspace_of(b.s, d);
+  char* ws = static_cast<char*>(workspace);
+  return AttnArgs{b,         q,
+                  scale,     window,
+                  o,         lse,
+                  d.workers, d.run_tiles, d.row_blocks,
+                  d.rows,    reinterpret_cast<int64_t*>(ws),
+                  reinterpret_cast<int32_t*>(ws + L.bad), reinterpret_cast<f32x2*>(ws + L.ml),
+                  reinterpret_cast<float*>(ws + L.o)};
+}
+
+// The join after an attention kernel: about 2048 workgroups at most, a query
+// row or more to each.
+template <int DV, typename TIn>
+hipError_t run_join(const AttnArgs& a, hipStream_t st) {
+  if (a.workers == 1) return hipSuccess;
+  const kda_kv_shape& s = a.kb.s;
+  const int rows = s.T * (s.Hq / s.Hkv);
+  const int64_t wanted = ((int64_t)s.B * s.Hkv * rows + 2047) / 2048;
+  const int each = wanted > rows ? rows : (int)wanted;
+  hipLaunchKernelGGL((join_kernel<DV, TIn>), dim3(s.B, s.Hkv, (rows + each - 1) / each), dim3(DV / 4 * kJoinGroups), 0,
+                     st, a, each);
+  return hipGetLastError();
 }
 
 }  // namespace
