@@ -608,7 +608,7 @@ kda_status kda_kv_append(const kda_kv_shape* shape, const kda_pages* pages, cons
  * the cache, so they are appended first.  A row that sees no token (p < 0)
  * gets o = 0 and lse = -inf.  Tokens that a row does not see do not reach it,
  * whatever they hold.  1 <= T <= 16 (a decode token, or the drafts of a
- * speculative round).  scale normally 1/sqrt of the width the model trained
+ * speculative round), B * max_pages * page_size at most about 2^35 tokens.  scale normally 1/sqrt of the width the model trained
  * with; it must be finite.
  * A sequence whose visible tokens run past the page table or lie on a page
  * outside [0, n_pages) sets KDA_DEV_ERR_PAGE and is skipped.

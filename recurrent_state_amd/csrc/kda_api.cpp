@@ -141,6 +141,11 @@ kda_status check_kv_shape(const kda_kv_shape* s, const kda_pages* pages, int32_t
   return KDA_OK;
 }
 
+// kda_attn_decode counts the tiles (32 tokens or more) of all sequences in 32 bits.
+bool attends(const kda_kv_shape& s, int32_t page_size, int32_t max_pages) {
+  return s.T <= kMaxT && (int64_t)s.B * ((int64_t)max_pages * page_size / 32 + 2) <= (int64_t)1 << 30;
+}
+
 // Everything the two calls share; fills in `b` on success.
 kda_status check_kv(const kda_kv_shape* s, const kda_pages* pages, const int32_t* table, int32_t max_pages,
                     const int32_t* tok_start, int32_t n_tokens, const int64_t* pos, int32_t* dev_err,
@@ -693,7 +698,7 @@ kda_status kda_attn_decode(const kda_kv_shape* shape, const kda_pages* pages, co
   kda::KvBatch b;
   kda_status r = check_kv(shape, pages, table, max_pages, tok_start, n_tokens, pos, dev_err, &b);
   if (r != KDA_OK) return r;
-  if (shape->T > kMaxT || window < 0 || !isfinite(scale)) return KDA_ERR_SHAPE;
+  if (!attends(*shape, pages->page_size, max_pages) || window < 0 || !isfinite(scale)) return KDA_ERR_SHAPE;
   kda::KvRows qr{q, q_stride};
   if ((r = check_rows(*shape, shape->Hq, shape->dk, &qr)) != KDA_OK) return r;
   if (b.s.B == 0 || n_tokens == 0) return KDA_OK;
@@ -706,7 +711,7 @@ kda_status kda_attn_decode(const kda_kv_shape* shape, const kda_pages* pages, co
 }
 
 size_t kda_attn_workspace_bytes(const kda_kv_shape* shape, const kda_pages* pages, int32_t max_pages) {
-  if (check_kv_shape(shape, pages, max_pages) != KDA_OK || shape->T > kMaxT) return 0;
+  if (check_kv_shape(shape, pages, max_pages) != KDA_OK || !attends(*shape, pages->page_size, max_pages)) return 0;
   return kda::attn_workspace_bytes(*shape, pages->page_size, max_pages);
 }
 

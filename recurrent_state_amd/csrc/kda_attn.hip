@@ -320,16 +320,14 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
   const int wave = uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int hk = blockIdx.y, rb = blockIdx.z, worker = blockIdx.x;
   const int G = kb.s.Hq / kb.s.Hkv;
-  const Run run = find_run<TILE>(a, worker, worker == 0 && hk == 0 && rb == 0 && wave == 0);
+  Run<TILE> run(a, worker, worker == 0 && hk == 0 && rb == 0 && wave == 0);
   float x_scale = a.scale * kLog2e;
   if (sizeof(TC) == 1) x_scale *= kb.pages.k_scale[hk];
   const float v_scale = sizeof(TC) == 1 ? kb.pages.v_scale[hk] : 1.f;
 
-  int64_t tile = run.tile, first = run.first;
-  for (int b = run.b; tile < run.end && b < kb.s.B; ++b) {
-    const Seq s = uniform_seq<TILE>(a, b);
-    if (s.tiles == 0) continue;
-    const int64_t stop = min(run.end, first + s.tiles);
+  while (run.tile < run.end) {
+    const Seq& s = run.s;
+    const int32_t tile = run.tile, first = run.first, stop = min(run.end, first + s.tiles);
     const int R = s.n * G;
     if (rb * 16 * NQ < R) {
       // Queries, and the last visible token of the lane's row in each block.
@@ -355,12 +353,12 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
 
       // This wave's tokens: t0, t0 + TILE, ... below `past`.
       const int base = (s.lo & ~(TILE - 1)) + wave * SUB;
-      int t0 = base + (int)(tile - first) * TILE;
-      const int past = min(s.end, base - wave * SUB + (int)(stop - first) * TILE);
+      int t0 = base + (tile - first) * TILE;
+      const int past = min(s.end, base - wave * SUB + (stop - first) * TILE);
       // Tokens below all_lo or past the first row's are hidden from some row.
       const int all_lo = a.window > 0 ? max((int)(s.pos + s.n) - a.window, 0) : 0;
       C cache;
-      PageWalk walk(kb, s, b, hk);
+      PageWalk walk(kb, s, run.b, hk);
       const TC* const pages_k = static_cast<const TC*>(kb.pages.k);
       const TC* const pages_v = static_cast<const TC*>(kb.pages.v);
       int32_t id[GROUPS];  // page entries of the tile to be loaded next
@@ -540,8 +538,7 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
         __syncthreads();
       }
     }
-    first += s.tiles;
-    tile = stop;
+    run.next(stop);
   }
 }
 

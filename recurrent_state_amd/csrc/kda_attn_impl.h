@@ -36,9 +36,9 @@ struct AttnArgs {
   int32_t run_tiles;   // tiles of a run at least, while there are enough
   int32_t row_blocks;  // blocks of query rows of a (sequence, kv head)
   int32_t rows;        // query rows of a block
-  // Workspace: first tile of each sequence [B + 1], then for every piece
+  // Workspace: each sequence's first and last worker [B], then for every piece
   // (worker, slot, kv head, row block) a flag, (max, sum) and output rows.
-  int64_t* first_tile;
+  int2* span;
   int32_t* piece_bad;
   f32x2* piece_ml;
   float* piece_o;
@@ -60,13 +60,8 @@ __device__ __forceinline__ float max_over_rows(float x) {
   return fmaxf(a, b);
 }
 
-// A value that every lane holds, moved to scalar registers.
+// A value that every lane holds, moved to a scalar register.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-__device__ __forceinline__ int64_t uniform(int64_t x) {
-  const uint32_t lo = (uint32_t)uniform((int)(uint32_t)x), hi = (uint32_t)uniform((int)(x >> 32));
-  return (int64_t)((uint64_t)hi << 32 | lo);
-}
-
 // x, as a value that the compiler knows nothing of: what is computed from it
 // stays where it is used, instead of being hoisted out of the loops around
 // and held in registers (or spilled) for all of them.
@@ -89,101 +84,148 @@ struct Seq {
 template <int TILE>
 __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
   const KvBatch& kb = a.kb;
+  const int64_t pos = kb.pos[b];  // asked for together with the token range
   const SeqRows sr = seq_rows(kb, b);
-  Seq s{sr.row0, sr.n, 0, 0, 0, 0, sr.bad ? KDA_DEV_ERR_TOKENS : 0};
+  Seq s{sr.row0, sr.n, pos, 0, 0, 0, sr.bad ? KDA_DEV_ERR_TOKENS : 0};
   if (sr.n == 0) return s;
-  s.pos = kb.pos[b];
-  const int64_t end = s.pos + sr.n;
-  if (s.pos > (int64_t)1 << 30 || end > ((int64_t)kb.max_pages << kb.page_shift)) {
+  const int64_t end = pos + sr.n;
+  if (pos > (int64_t)1 << 30 || end > ((int64_t)kb.max_pages << kb.page_shift)) {
     s.err = KDA_DEV_ERR_PAGE;
     return s;
   }
   s.tiles = 1;
   if (end > 0) {
     s.end = (int32_t)end;
-    if (a.window > 0 && s.pos + 1 > a.window) s.lo = (int32_t)(s.pos + 1 - a.window);
+    if (a.window > 0 && pos + 1 > a.window) s.lo = (int32_t)(pos + 1 - a.window);
     s.tiles = (s.end - (s.lo & ~(TILE - 1)) + TILE - 1) / TILE;
   }
   return s;
 }
 
-// The same for a sequence that the whole wave works on.
-template <int TILE>
-__device__ __forceinline__ Seq uniform_seq(const AttnArgs& a, int b) {
-  Seq s = seq_of<TILE>(a, b);
-  s.row0 = uniform(s.row0);
-  s.n = uniform(s.n);
-  s.pos = uniform(s.pos);
-  s.lo = uniform(s.lo);
-  s.end = uniform(s.end);
-  s.tiles = uniform(s.tiles);
+// Lane `from`'s sequence, in scalar registers.
+__device__ __forceinline__ Seq seq_of_lane(const Seq& x, int from) {
+  Seq s;
+  s.row0 = __builtin_amdgcn_readlane(x.row0, from);
+  s.n = __builtin_amdgcn_readlane(x.n, from);
+  s.pos = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x.pos >> 32), from) << 32 |
+                    (uint32_t)__builtin_amdgcn_readlane((int)x.pos, from));
+  s.lo = __builtin_amdgcn_readlane(x.lo, from);
+  s.end = __builtin_amdgcn_readlane(x.end, from);
+  s.tiles = __builtin_amdgcn_readlane(x.tiles, from);
+  s.err = 0;
   return s;
 }
 
 // Inclusive sum over the wave's lanes.
-__device__ __forceinline__ int64_t wave_scan(int64_t x) {
+__device__ __forceinline__ int32_t wave_scan(int32_t x) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int d = 1; d < kWave; d *= 2) {
-    const int64_t y = __shfl_up(x, d);
+    const int32_t y = __shfl_up(x, d);
     if (lane >= d) x += y;
   }
   return x;
 }
 
-// A worker's run [tile, end) of the tile list and where it begins: in
-// sequence b, whose own tiles begin at `first`.
-struct Run {
-  int64_t tile, end, first;
-  int b;
+// How `total` tiles fall to the workers: `count` of them have a run (none is
+// empty), the first `more` of one tile more than the others' `each`.
+struct Shares {
+  uint32_t count, each, more;
+
+  __device__ __forceinline__ Shares(const AttnArgs& a, uint32_t total) {
+    const uint32_t most = (total + a.run_tiles - 1) / a.run_tiles;
+    count = most < (uint32_t)a.workers ? most : a.workers;
+    each = count ? total / count : 0;
+    more = total - each * count;
+  }
+  __device__ __forceinline__ uint32_t begin(uint32_t worker) const { return worker * each + min(worker, more); }
+  // The worker that has tile x.
+  __device__ __forceinline__ uint32_t of(uint32_t x) const {
+    const uint32_t y = more * (each + 1);
+    return x < y ? x / (each + 1) : more + (x - y) / each;
+  }
 };
 
-// Workers with something to do: no run is empty.
-__device__ __forceinline__ int64_t busy_workers(const AttnArgs& a, int64_t total) {
-  const int64_t most = (total + a.run_tiles - 1) / a.run_tiles;
-  return most < a.workers ? most : a.workers;
-}
-
-// Called by a whole wave.  `record`: this wave also names refused sequences
-// and writes the sequences' first tiles for the join.
+// A worker's run [tile, end) of the tile list, and the sequence that it is at:
+// number b, whose own tiles begin at `first`.
 template <int TILE>
-__device__ __forceinline__ Run find_run(const AttnArgs& a, int worker, bool record) {
-  const int lane = threadIdx.x & 63, B = a.kb.s.B;
-  int64_t total = 0, upto = 0;
-  int32_t tiles = 0;
-  for (int c = 0; c < B; c += kWave) {
-    Seq s{};
-    if (c + lane < B) s = seq_of<TILE>(a, c + lane);
-    tiles = s.tiles;
-    upto = wave_scan(tiles);
-    if (record && c + lane < B) {
-      a.first_tile[c + lane] = total + upto - tiles;
-      if (s.err) set_err(a.kb.dev_err, s.err);
+struct Run {
+  const AttnArgs& a;
+  int32_t tile, end, first;
+  int b;
+  Seq s;
+
+  // Called by a whole wave.  `record`: this wave also names refused sequences
+  // and writes the sequences' workers for the join.
+  __device__ __forceinline__ Run(const AttnArgs& args, int worker, bool record)
+      : a(args), tile(0), end(0), first(0), b(0), s{} {
+    const int lane = threadIdx.x & 63, B = a.kb.s.B;
+    Seq lanes{};  // 64 sequences, one to a lane
+    int32_t total = 0, upto = 0;
+    for (int c = 0; c < B; c += kWave) {
+      lanes = c + lane < B ? seq_of<TILE>(a, c + lane) : Seq{};
+      upto = wave_scan(lanes.tiles);
+      if (record && lanes.err) set_err(a.kb.dev_err, lanes.err);
+      total += __builtin_amdgcn_readlane(upto, kWave - 1);
     }
-    total += uniform(__shfl(upto, kWave - 1));
-  }
-  if (record && lane == 0) a.first_tile[B] = total;
-  const int64_t w = busy_workers(a, total);
-  if (worker >= w) return Run{0, 0, 0, 0};
-  Run r{worker * total / w, (worker + 1) * total / w, 0, 0};
-  // The chunk that holds r.tile: with up to 64 sequences the one at hand.
-  int c = 0;
-  int64_t before = 0;
-  if (B > kWave) {
-    for (; c < B; c += kWave) {
-      tiles = c + lane < B ? seq_of<TILE>(a, c + lane).tiles : 0;
-      upto = wave_scan(tiles);
-      const int64_t sum = uniform(__shfl(upto, kWave - 1));
-      if (before + sum > r.tile) break;
-      before += sum;
+    const Shares shares(a, total);
+    if (worker < (int)shares.count) {
+      tile = shares.begin(worker);
+      end = shares.begin(worker + 1);
     }
+    // The chunk that holds `tile`: with up to 64 sequences the one at hand.
+    int32_t before = 0;
+    if (B > kWave) {
+      for (; b < B; b += kWave) {
+        lanes = b + lane < B ? seq_of<TILE>(a, b + lane) : Seq{};
+        upto = wave_scan(lanes.tiles);
+        const int32_t sum = __builtin_amdgcn_readlane(upto, kWave - 1);
+        if (record) write_span(shares, b + lane, before + upto, lanes.tiles);
+        // The recording wave goes through all of them; its worker is the first.
+        if (before + sum > tile && !record) break;
+        before += sum;
+      }
+      if (record) {
+        b = before = 0;
+        if (tile < end) {  // back to the first sequence with tiles
+          for (; b < B; b += kWave) {
+            lanes = b + lane < B ? seq_of<TILE>(a, b + lane) : Seq{};
+            upto = wave_scan(lanes.tiles);
+            if (__builtin_amdgcn_readlane(upto, kWave - 1) > 0) break;
+          }
+        }
+      }
+    } else if (record) {
+      write_span(shares, lane, upto, lanes.tiles);
+    }
+    if (tile >= end) return;
+    // The first lane whose tiles reach past `tile`.
+    const int at = uniform(__ffsll((unsigned long long)__ballot(before + upto > tile)) - 1);
+    b += at;
+    first = before + __builtin_amdgcn_readlane(upto - lanes.tiles, at);
+    s = seq_of_lane(lanes, at);
   }
-  // The first lane whose tiles reach past r.tile.
-  const int at = __ffsll((unsigned long long)__ballot(before + upto > r.tile)) - 1;
-  r.b = c + at;
-  r.first = before + uniform(__shfl(upto - tiles, at));
-  return r;
-}
+
+  // Sequence `seq`, whose tiles end before tile `upto`.
+  __device__ __forceinline__ void write_span(const Shares& shares, int seq, int32_t upto, int32_t tiles) const {
+    if (seq < a.kb.s.B)
+      a.span[seq] = tiles > 0 ? make_int2(shares.of(upto - tiles), shares.of(upto - 1)) : make_int2(0, 0);
+  }
+
+  // Past the sequence's tiles that end at `stop`.
+  __device__ __forceinline__ void next(int32_t stop) {
+    tile = stop;
+    first += s.tiles;
+    if (tile >= end) return;
+    do {
+      if (++b >= a.kb.s.B) {  // only if the positions change under the call
+        tile = end;
+        return;
+      }
+      s = seq_of_lane(seq_of<TILE>(a, b), 0);
+    } while (s.tiles == 0);
+  }
+};
 
 // Where the visible tokens of one sequence are, for a wave that walks them in
 // groups of 16 (which no page splits).  Table entries come through the scalar
@@ -235,65 +277,74 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
 // Joins the pieces of the sequences that more than one worker had a part of:
 // with m the largest of the pieces' maxima,
 //   o = sum_w 2^(m_w - m) o_w / sum_w 2^(m_w - m) l_w.
-// One workgroup takes `rows_each` query rows of a (sequence, kv head).  Every
-// wave finds m and the sum by itself, a piece to a lane; then DV / 4 lanes hold
-// a row, eight groups of them read pieces at once, and their sums meet in LDS.
-constexpr int kJoinGroups = 8;
+// DV / 4 lanes hold a row of outputs, and a workgroup has four to sixteen such
+// groups.
+// `split` of them (a power of two) share a row, each with every split-th
+// piece, so that a long sequence's many pieces are read side by side, and a
+// batch's few pieces of many rows are too; a workgroup takes `rows_each` query
+// rows of a (sequence, kv head).  Every wave finds m and the sum by itself, a
+// piece to a lane.
+template <int DV>
+constexpr int kJoinGroups = DV == 512 ? 4 : DV == 128 ? 8 : 16;
 
 template <int DV, typename TIn>
-__global__ void __launch_bounds__(DV / 4 * kJoinGroups) join_kernel(AttnArgs a, int rows_each) {
+__global__ void __launch_bounds__(DV / 4 * kJoinGroups<DV>) join_kernel(AttnArgs a, int rows_each, int split) {
   constexpr int LANES = DV / 4;
-  __shared__ f32x4 part[kJoinGroups][LANES];
+  __shared__ f32x4 part[kJoinGroups<DV>][LANES];
   const KvBatch& kb = a.kb;
   const int b = blockIdx.x, hk = blockIdx.y;
-  const int64_t first = a.first_tile[b], past = a.first_tile[b + 1], total = a.first_tile[kb.s.B];
-  if (past == first) return;
-  // The worker whose run holds tile x: the last one that begins at or before it.
-  const int64_t busy = busy_workers(a, total);
-  const int w0 = (int)(((first + 1) * busy - 1) / total);
-  const int w1 = (int)((past * busy - 1) / total);
+  const int w0 = a.span[b].x, w1 = a.span[b].y;
   if (w0 == w1) return;
   const int G = kb.s.Hq / kb.s.Hkv;
   const SeqRows sr = seq_rows(kb, b);
-  const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES, wl = threadIdx.x & 63;
+  constexpr int SAME = LANES < kWave ? LANES : kWave;  // lanes of a wave that hold one row
+  const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES, same = threadIdx.x % SAME;
+  const int share = group & (split - 1), rows_at_once = kJoinGroups<DV> / split;
   const int r0 = blockIdx.z * rows_each, r1 = min(r0 + rows_each, sr.n * G);
+  if (r0 >= r1) return;
+  // Refused (every row block of a worker met the same pages): nothing is written.
+  int bad = 0;
+  for (int w = w0 + threadIdx.x; w <= w1; w += blockDim.x)
+    bad |= a.piece_bad[piece_index(a, w, w == w0 ? 1 : 0, hk, r0 / a.rows)];
+  if (__syncthreads_or(bad)) return;
   const float vs = kb.pages.v_scale ? kb.pages.v_scale[hk] : 1.f;
-  for (int r = r0; r < r1; ++r) {
+  for (int rr = r0; rr < r1; rr += rows_at_once) {
+    const bool live = rr + group / split < r1;
+    const int r = live ? rr + group / split : r0;
     const int rb = r / a.rows, in = r % a.rows;
+    const auto row_of = [&](int w) { return piece_index(a, w, w == w0 ? 1 : 0, hk, rb) * a.rows + in; };
     float m = -INFINITY, l = 0.f;
-    bool bad = false;
-    for (int w = w0 + wl; w <= w1; w += kWave) {
-      const int64_t at = piece_index(a, w, w == w0 ? 1 : 0, hk, rb);
-      bad |= a.piece_bad[at] != 0;
-      m = fmaxf(m, a.piece_ml[at * a.rows + in][0]);
-    }
-    if (__ballot(bad) != 0) return;  // refused: the whole workgroup sees it
+    for (int w = w0 + same; w <= w1; w += SAME) m = fmaxf(m, a.piece_ml[row_of(w)][0]);
 #pragma unroll
-    for (int d = 1; d < kWave; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
+    for (int d = 1; d < SAME; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
     // A piece in which the row sees no token has m = -inf and zeros.
     const float top = m == -INFINITY ? 0.f : m;
-    for (int w = w0 + wl; w <= w1; w += kWave) {
-      const f32x2 ml = a.piece_ml[piece_index(a, w, w == w0 ? 1 : 0, hk, rb) * a.rows + in];
+    for (int w = w0 + same; w <= w1; w += SAME) {
+      const f32x2 ml = a.piece_ml[row_of(w)];
       l += ml[1] * exp2_(ml[0] - top);
     }
 #pragma unroll
-    for (int d = 1; d < kWave; d *= 2) l += __shfl_xor(l, d);
+    for (int d = 1; d < SAME; d *= 2) l += __shfl_xor(l, d);
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int w = w0 + group; w <= w1; w += kJoinGroups) {
-      const int64_t row = piece_index(a, w, w == w0 ? 1 : 0, hk, rb) * a.rows + in;
+    for (int w = w0 + share; w <= w1; w += split) {
+      const int64_t row = row_of(w);
       const float f = exp2_(a.piece_ml[row][0] - top);
       const f32x4 x = *reinterpret_cast<const f32x4*>(a.piece_o + row * DV + 4 * lane);
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] += x[i] * f;
     }
-    part[group][lane] = o;
-    __syncthreads();
-    if (group == 0) {
+    if (split > 1) {
+      part[group][lane] = o;
+      __syncthreads();
+      for (int g = 1; g < split; ++g) {
+        const f32x4 x = part[group - share + (share + g & (split - 1))][lane];
 #pragma unroll
-      for (int g = 1; g < kJoinGroups; ++g)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] += part[g][lane][i];
+        for (int i = 0; i < 4; ++i) o[i] += x[i];
+      }
+      __syncthreads();
+    }
+    if (live && share == 0) {
       const float inv = l == 0.f ? 0.f : vs / l;
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] *= inv;
@@ -301,7 +352,6 @@ __global__ void __launch_bounds__(DV / 4 * kJoinGroups) join_kernel(AttnArgs a, 
       store4(static_cast<TIn*>(a.o) + row * DV + 4 * lane, o);
       if (a.lse && lane == 0) a.lse[row] = (m + __log2f(l)) * kLn2;
     }
-    __syncthreads();
   }
 }
 
@@ -326,7 +376,7 @@ struct Workspace {
 inline Workspace workspace_of(const kda_kv_shape& s, const Split& d) {
   const size_t pieces = (size_t)d.workers * 2 * s.Hkv * d.row_blocks;
   Workspace L;
-  L.bad = round_up(((size_t)s.B + 1) * 8, 256);
+  L.bad = round_up((size_t)s.B * 8, 256);
   L.ml = round_up(L.bad + pieces * 4, 256);
   L.o = round_up(L.ml + pieces * d.rows * 8, 256);
   L.total = round_up(L.o + pieces * d.rows * s.dv * 4, 256);
@@ -341,22 +391,26 @@ inline AttnArgs make_args(const KvBatch& b, KvRows q, float scale, int32_t windo
                   scale,     window,
                   o,         lse,
                   d.workers, d.run_tiles, d.row_blocks,
-                  d.rows,    reinterpret_cast<int64_t*>(ws),
+                  d.rows,    reinterpret_cast<int2*>(ws),
                   reinterpret_cast<int32_t*>(ws + L.bad), reinterpret_cast<f32x2*>(ws + L.ml),
                   reinterpret_cast<float*>(ws + L.o)};
 }
 
-// The join after an attention kernel: about 2048 workgroups at most, a query
-// row or more to each.
+// The join after an attention kernel.  A sequence has about workers / B pieces
+// (the lengths are not known here): a row's groups of lanes are at most half as
+// many, and a workgroup takes rows enough that about 2048 of them cover all.
 template <int DV, typename TIn>
 hipError_t run_join(const AttnArgs& a, hipStream_t st) {
   if (a.workers == 1) return hipSuccess;
   const kda_kv_shape& s = a.kb.s;
   const int rows = s.T * (s.Hq / s.Hkv);
-  const int64_t wanted = ((int64_t)s.B * s.Hkv * rows + 2047) / 2048;
-  const int each = wanted > rows ? rows : (int)wanted;
-  hipLaunchKernelGGL((join_kernel<DV, TIn>), dim3(s.B, s.Hkv, (rows + each - 1) / each), dim3(DV / 4 * kJoinGroups), 0,
-                     st, a, each);
+  int split = kJoinGroups<DV>;
+  while (split > 1 && (int64_t)split * 2 * s.B > a.workers) split /= 2;
+  const int at_once = kJoinGroups<DV> / split;
+  int64_t each = ((int64_t)s.B * s.Hkv * rows + 2047) / 2048;
+  each = (each + at_once - 1) / at_once * at_once;
+  hipLaunchKernelGGL((join_kernel<DV, TIn>), dim3(s.B, s.Hkv, (unsigned)((rows + each - 1) / each)),
+                     dim3(DV / 4 * kJoinGroups<DV>), 0, st, a, (int)each, split);
   return hipGetLastError();
 }
 

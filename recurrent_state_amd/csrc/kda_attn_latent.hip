@@ -8,27 +8,27 @@
 // its waves and for both uses.  A workgroup of eight waves takes up to 128
 // query rows and walks its run in tiles of 32 tokens:
 //
-//   scores   S^T = K Q^T.  A wave has 16 or 32 query rows, half of the
-//            contraction (every other 32 values) and, with few rows, half of
-//            the tokens; its queries stay in registers (36 or 72).  The halves
-//            go to the LDS as they leave the MFMA.
-//   softmax  a wave takes 16 rows: sums the halves, moves the maximum and
-//            leaves the probabilities in the LDS as an MFMA operand.
-//   output   O^T += V^T P^T.  A wave has 64 of the 512 columns of all rows (32
-//            to 128 registers), so a value is read from the LDS once.  V^T
+//   scores   S^T = K Q^T and their softmax.  One wave for each 16 query rows,
+//            whose queries it holds (72 registers): the rows' maxima and sums
+//            stay in its registers, and the probabilities go to the LDS as an
+//            MFMA operand.
+//   output   O^T += V^T P^T.  Every wave has 64 of the 512 columns of all rows
+//            (32 to 128 registers), so a value is read from the LDS once.  V^T
 //            comes from ds_read_b64_tr_b16, which hands lane l column l & 15
 //            of four rows.
 //
-// Scores of tile i + 1 and output of tile i are one phase between barriers,
-// the softmax the other; later tiles are on their way meanwhile (LDS-direct
-// loads, 16 bytes a lane).  The split by contraction and columns is what keeps
-// a wave within 256 registers, two waves to a SIMD; waves with 32 whole rows
-// each (256 + 144 registers) spilled.
+// Between two barriers the waves score tile i + 1 and weigh tile i, while later
+// tiles are on their way (LDS-direct loads, 16 bytes a lane).  So the two waves
+// of a SIMD fill each other's waits: a form with the scores' contraction split
+// over pairs of waves, which halves the key reads but needs a second barrier
+// and an exchange in the LDS for every tile, took 3.2 us a tile of 128 rows.
 //
-// LDS layout: 16-byte chunk c of row r lies at chunk (c & ~7) | ((c ^ f(r)) &
-// 7) of its row, f(r) = 2 (r / 2 % 4) + r / 8 % 2: the key reads (16 rows, one
-// chunk) and the transposed value reads (8 rows, two neighbouring chunks) both
-// touch every bank once.
+// LDS layout of a tile: 32 rows of 64 16-byte chunks (the values), then 32 rows
+// of the last 8.  Chunk c of row r lies at c ^ f(r), f(r) = r's four bits
+// rotated left by one, in the first part, and at c ^ (r / 2 % 8) in the second:
+// the key reads (16 rows, one chunk) and the transposed value reads (8 rows,
+// two neighbouring chunks) touch every bank once, and a row's first part is one
+// load of a wave, whose addresses are the row's and a constant of the lane.
 //
 // The outputs are scaled only when a row's maximum has grown past 2^8 times
 // the one in use: probabilities stay below 2^8 and their roundings are
@@ -42,19 +42,20 @@ namespace {
 
 constexpr int kDk = 576, kDv = 512;
 constexpr int kWaves = 8, kTile = 32;       // tokens
-constexpr int kRowBytes = kDk * 2;          // 72 chunks of 16 bytes
-constexpr int kBufBytes = kTile * kRowBytes;
-constexpr int kHalf = 16 * kRowBytes;       // 16 rows
-constexpr int kSteps = kDk / 64;            // contraction steps of a wave
+constexpr int kRowBytes = kDk * 2;          // in the pages: 72 chunks of 16 bytes
+constexpr int kMain = kDv * 2, kTail = kRowBytes - kMain;  // in the LDS: see above
+constexpr int kTailAt = kTile * kMain, kBufBytes = kTile * kRowBytes;
+constexpr int kSteps = kDk / 32;            // contraction steps
 constexpr int kCols = kDv / kWaves / 16;    // column tiles of a wave
-constexpr int kLoads = 9;                   // LDS-direct loads of a loading wave and tile
 
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) void lds_void;
 typedef const __attribute__((address_space(1))) void global_void;
 
-__device__ __forceinline__ int swizzle(int row) { return (row >> 1 & 3) << 1 | (row >> 3 & 1); }
+// By row of 16.
+__device__ __forceinline__ int swizzle(int row) { return (row << 1 & 15) | (row >> 3 & 1); }
+__device__ __forceinline__ int swizzle_tail(int row) { return row >> 1 & 7; }
 
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -71,132 +72,122 @@ __device__ __forceinline__ void lds_barrier() {
 template <int RB>
 __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
   // Tiles in the LDS: one being scored, one being weighed, the others on
-  // their way (what the scores and probabilities leave room for).
-  constexpr int BUFS = RB == 2 ? 4 : 3, AHEAD = BUFS - 1;
-  constexpr int QB = RB == 8 ? 2 : 1;   // row blocks whose scores a wave makes
-  constexpr int US = RB == 2 ? 1 : 2;   // 16-token groups of them
+  // their way (what the probabilities leave room for).
+  constexpr int BUFS = RB == 8 ? 3 : 4, AHEAD = BUFS - 1;
   __shared__ __attribute__((aligned(1024))) unsigned char lds[BUFS * kBufBytes];
-  __shared__ f32x4 lds_s[2][RB][2][kWave];     // scores: [contraction half][row block][16 tokens]
-  __shared__ u32x4 lds_p[RB][kWave];           // probabilities
-  __shared__ float lds_keep[RB][16];           // factor of the sums so far
+  __shared__ u32x4 lds_p[2][RB][kWave];        // probabilities, of even and odd tiles
+  __shared__ float lds_keep[2][RB][16];        // factors of the sums so far,
+  __shared__ int32_t lds_grown[2][RB];         // where some are not one
   __shared__ f32x2 lds_ml[RB][16];             // at the end: maximum, sum
 
   const KvBatch& kb = a.kb;
   const int wave = uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int rb = blockIdx.y, worker = blockIdx.x, Hq = kb.s.Hq;
-  const Run run = find_run<kTile>(a, worker, worker == 0 && rb == 0 && wave == 0);
+  Run<kTile> run(a, worker, worker == 0 && rb == 0 && wave == 0);
   const float x_scale = a.scale * kLog2e;
-  // The wave's part of the scores.
-  const int half = wave & 1, qb = (RB == 2 ? wave >> 2 : wave >> 1) * QB, us = RB == 2 ? wave >> 1 & 1 : 0;
 
-  // Byte offsets in a tile: key chunk 4 half + g of row `col` (of the wave's
-  // tokens), and the wave's value chunks of row 4 g + col / 4.  Computed where
-  // they are used (here()), as most lane constants below: registers are short.
-  auto k_at = [&] {
-    const int lane = here((int)threadIdx.x & 63), row = lane & 15;
-    return us * kHalf + row * kRowBytes + (((4 * half + (lane >> 4)) ^ swizzle(row)) & 7) * 16;
-  };
-  auto v_at = [&](int lane) {
-    const int row = 4 * (lane >> 4) + (lane >> 2 & 3);
-    return wave * 128 + row * kRowBytes + ((lane >> 1 & 1) ^ swizzle(row)) * 16 + (lane & 1) * 8;
-  };
+  // Byte offset in a tile of chunk c (below 16) of row `row`, for this wave's
+  // columns the chunks 8 (wave & 1) and on after chunk 16 (wave / 2).  Lane
+  // constants are computed where they are used (here()): registers are short.
+  auto chunk_at = [](int row, int c) { return row * kMain + ((c ^ swizzle(row & 15)) << 4); };
+  const int v_col = (wave >> 1) * 256, v_chunk = 8 * (wave & 1);
 
-  int64_t tile = run.tile, first = run.first;
-  for (int b = run.b; tile < run.end && b < kb.s.B; ++b) {
-    const Seq s = uniform_seq<kTile>(a, b);
-    if (s.tiles == 0) continue;
-    const int64_t stop = min(run.end, first + s.tiles);
+  while (run.tile < run.end) {
+    const Seq& s = run.s;
+    const int32_t tile = run.tile, first = run.first, stop = min(run.end, first + s.tiles);
     const int R = s.n * Hq, row0 = rb * RB * 16;
     if (row0 < R) {
-      bf16x8 q[QB][kSteps];
-#pragma unroll
-      for (int n = 0; n < QB; ++n) {
-        const int r = row0 + 16 * (qb + n) + (here(lane) & 15);
-        const bf16_t* p = static_cast<const bf16_t*>(a.q.p) + (int64_t)(s.row0 + r / Hq) * a.q.stride + r % Hq * kDk +
-                          32 * half + 8 * (here(lane) >> 4);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) q[n][k] = r < R ? *reinterpret_cast<const bf16x8*>(p + 64 * k) : bf16x8{};
-      }
+      bf16x8 q[kSteps];
       f32x4 out[RB][kCols];
 #pragma unroll
       for (int n = 0; n < RB; ++n)
 #pragma unroll
         for (int c = 0; c < kCols; ++c) out[n][c] = f32x4{};
-      float m = -INFINITY, l = 0.f;  // of the rows whose softmax the wave makes
+      float m = -INFINITY, l = 0.f;  // of the rows that the wave scores
       const int my_row = row0 + 16 * wave + (here(lane) & 15);
       const int vis = my_row < R ? (int)max(s.pos + my_row / Hq, (int64_t)-1) : -1;  // the last token it sees
 
-      const int n_tiles = s.end > 0 ? (int)(stop - tile) : 0;
-      const int tok0 = (s.lo & ~(kTile - 1)) + (int)(tile - first) * kTile;
+      const int n_tiles = s.end > 0 ? stop - tile : 0;
+      const int tok0 = (s.lo & ~(kTile - 1)) + (tile - first) * kTile;
       const int all_lo = a.window > 0 ? max((int)(s.pos + s.n) - a.window, 0) : 0;
       auto whole = [&](int t0) { return t0 >= all_lo && t0 + kTile - 1 <= s.pos; };
-      PageWalk walk(kb, s, b, 0);
+      PageWalk walk(kb, s, run.b, 0);
 
-      // Tile i into buffer i % BUFS.  Rows outside the visible tokens get a
-      // copy of the nearest visible one, so that a probability of zero meets
-      // what some row sees anyway.
-      const int t16 = 16 * (wave >> 1 & 1);
-      int32_t id = n_tiles > 0 ? walk.entry(tok0 + t16) : 0;  // of the tile to be loaded next
+      // Tile i into buffer i % BUFS: four rows to a wave, and eight rows' last
+      // chunks to waves 0 to 3.  Rows outside the visible tokens get a copy of
+      // the nearest visible one, so that a probability of zero meets what some
+      // row sees anyway.
+      const int t16 = 16 * (wave >> 2), tail16 = 16 * (wave >> 1 & 1);
+      int32_t id = 0, tail_id = 0;  // page entries of the tile to be loaded next
+      if (n_tiles > 0) id = walk.entry(tok0 + t16), tail_id = walk.entry(tok0 + tail16);
       auto load = [&](int i) {
-        if (wave >= 4) return;
-        const int tok = tok0 + i * kTile, at = tok + t16;
-        const unsigned char* base = static_cast<const unsigned char*>(kb.pages.k) + walk.row(at, id) * kRowBytes;
-        unsigned char* dst = lds + i % BUFS * kBufBytes + wave * (8 * kRowBytes);
-        const int from = min(max(at, walk.lo), walk.hi);  // the token of the base row
-        // Load k of a wave's 8 rows writes 64 chunks from chunk 64 k on; this
-        // lane's comes from row k - (lane < 8 k) of them.
-        const int lane_ = here(lane), r8 = 8 * (wave & 1);
+        const int tok = tok0 + i * kTile, lane = here((int)threadIdx.x & 63);
+        unsigned char* dst = lds + i % BUFS * kBufBytes;
+        const unsigned char* pages = static_cast<const unsigned char*>(kb.pages.k);
+        {
+          const unsigned char* base = pages + walk.row(tok + t16, id) * kRowBytes;
+          const int from = min(max(tok + t16, walk.lo), walk.hi);  // the token of the base row
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-          const int r = r8 + k - (lane_ < 8 * k), c = lane_ - 8 * k + (lane_ < 8 * k ? 72 : 0);
-          const int row = min(max(from + r, s.lo), s.end - 1) - from;
-          const uint32_t off = row * kRowBytes + ((c & ~7) | ((c ^ swizzle(r)) & 7)) * 16;
-          __builtin_amdgcn_global_load_lds((global_void*)(base + off), (lds_void*)(dst + k * 1024), 16, 0, 0);
+          for (int x = 0; x < 4; ++x) {
+            const int row = min(max(from + 4 * (wave & 3) + x, s.lo), s.end - 1) - from;
+            __builtin_amdgcn_global_load_lds(
+                (global_void*)(base + row * kRowBytes +
+                               (uint32_t)((lane ^ (8 * (wave & 1) | (wave >> 1 & 1))) * 16 ^ 32 * x)),
+                (lds_void*)(dst + (wave * 4 + x) * kMain), 16, 0, 0);
+          }
         }
-        id = walk.entry(at + kTile);
+        if (wave < 4) {
+          const unsigned char* base = pages + walk.row(tok + tail16, tail_id) * kRowBytes + kMain;
+          const int from = min(max(tok + tail16, walk.lo), walk.hi);
+          const int r = 8 * (wave & 1) + (lane >> 3), row = min(max(from + r, s.lo), s.end - 1) - from;
+          __builtin_amdgcn_global_load_lds(
+              (global_void*)(base + (uint32_t)(row * kRowBytes + ((lane & 7) ^ swizzle_tail(r)) * 16)),
+              (lds_void*)(dst + kTailAt + wave * 8 * kTail), 16, 0, 0);
+        }
+        id = walk.entry(tok + kTile + t16);
+        tail_id = walk.entry(tok + kTile + tail16);
       };
       // Waits until tile i has landed; tiles up to `issued` are on their way.
       auto landed = [&](int i, int issued) {
-        if (BUFS == 4 && issued - i >= 2)
-          wait_loads<2 * kLoads>();
-        else if (issued - i >= 1)
-          wait_loads<kLoads>();
-        else
-          wait_loads<0>();
+        const int behind = issued - i;
+        if (wave < 4) {
+          if (BUFS == 4 && behind >= 2)
+            wait_loads<10>();
+          else if (behind >= 1)
+            wait_loads<5>();
+          else
+            wait_loads<0>();
+        } else {
+          if (BUFS == 4 && behind >= 2)
+            wait_loads<8>();
+          else if (behind >= 1)
+            wait_loads<4>();
+          else
+            wait_loads<0>();
+        }
       };
 
+      // Scores and probabilities of tile i, for the waves that have rows.
       auto scores = [&](int i) {
-        const unsigned char* buf = lds + i % BUFS * kBufBytes + k_at();
-        f32x4 x[QB][US];
-#pragma unroll
-        for (int n = 0; n < QB; ++n)
-#pragma unroll
-          for (int u = 0; u < US; ++u) x[n][u] = f32x4{};
+        if (wave >= RB) return;
+        const int t0 = tok0 + i * kTile, lane = here((int)threadIdx.x & 63), g = lane >> 4, row = lane & 15;
+        const unsigned char* buf = lds + i % BUFS * kBufBytes;
+        f32x4 p[2] = {f32x4{}, f32x4{}};
 #pragma unroll
         for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-          for (int u = 0; u < US; ++u) {
-            const bf16x8 key = *reinterpret_cast<const bf16x8*>(buf + k * 128 + u * kHalf);
-#pragma unroll
-            for (int n = 0; n < QB; ++n) x[n][u] = mfma_bf16(key, q[n][k], x[n][u]);
+          for (int u = 0; u < 2; ++u) {
+            // Key chunk 4 k + g.
+            const unsigned char* at =
+                k < 16 ? buf + chunk_at(row, 4 * (k & 3) + g) + (k >> 2) * 256 + u * 16 * kMain
+                       : buf + kTailAt + (16 * u + row) * kTail + ((4 * (k & 1) + g ^ swizzle_tail(row)) << 4);
+            p[u] = mfma_bf16(*reinterpret_cast<const bf16x8*>(at), q[k], p[u]);
           }
-#pragma unroll
-        for (int n = 0; n < QB; ++n)
-#pragma unroll
-          for (int u = 0; u < US; ++u) lds_s[half][qb + n][us + u][lane] = x[n][u];
-      };
-
-      auto softmax = [&](int i) {
-        if (wave >= RB) return;
-        const int t0 = tok0 + i * kTile, lane = here((int)threadIdx.x & 63), g = lane >> 4;
-        f32x4 p[2];
         float top = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const f32x4 x = lds_s[0][wave][u][lane], y = lds_s[1][wave][u][lane];
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) p[u][j] = (x[j] + y[j]) * x_scale;
-        }
+          for (int j = 0; j < 4; ++j) p[u][j] *= x_scale;
         if (!whole(t0)) {
           const int low = a.window > 0 ? vis - a.window : -1;
 #pragma unroll
@@ -226,23 +217,27 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
             p[u][j] = exp2_(p[u][j] - mu);
             l += p[u][j];
           }
-        lds_p[wave][lane] = (u32x4){pack2(p[0][0], p[0][1]), pack2(p[0][2], p[0][3]), pack2(p[1][0], p[1][1]),
-                                    pack2(p[1][2], p[1][3])};
-        if (g == 0) lds_keep[wave][lane] = keep;
+        lds_p[i & 1][wave][lane] = (u32x4){pack2(p[0][0], p[0][1]), pack2(p[0][2], p[0][3]), pack2(p[1][0], p[1][1]),
+                                           pack2(p[1][2], p[1][3])};
+        const bool grown = __ballot(keep != 1.f) != 0;
+        if (grown && g == 0) lds_keep[i & 1][wave][lane] = keep;
+        if (lane == 0) lds_grown[i & 1][wave] = grown;
       };
 
       auto output = [&](int i) {
         const int t0 = tok0 + i * kTile, lane = here((int)threadIdx.x & 63);
         const unsigned char* buf = lds + i % BUFS * kBufBytes;
+        const uint64_t grown = __ballot(lane < RB && lds_grown[i & 1][lane % RB] != 0);
+        if (grown != 0) {
 #pragma unroll
-        for (int n = 0; n < RB; ++n) {
-          const float keep = lds_keep[n][lane & 15];
-          if (__ballot(keep != 1.f) != 0) {
+          for (int n = 0; n < RB; ++n)
+            if (grown >> n & 1) {
+              const float keep = lds_keep[i & 1][n][lane & 15];
 #pragma unroll
-            for (int c = 0; c < kCols; ++c)
+              for (int c = 0; c < kCols; ++c)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) out[n][c][j] *= keep;
-          }
+                for (int j = 0; j < 4; ++j) out[n][c][j] *= keep;
+            }
         }
         // A probability of zero must meet a finite value: look at the tokens
         // that only some rows see, in this wave's columns.
@@ -251,7 +246,7 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int j = t0 + 8 * x + (lane >> 3);
-            const u32x4 v = *reinterpret_cast<const u32x4*>(buf + (j - t0) * kRowBytes + wave * 128 + (lane & 7) * 16);
+            const u32x4 v = *reinterpret_cast<const u32x4*>(buf + v_col + chunk_at(j - t0, v_chunk + (lane & 7)));
             uint32_t peak = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) peak = max(peak, max(v[e] << 16 & 0x7fff0000u, v[e] & 0x7fff0000u));
@@ -259,12 +254,12 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
           }
         }
         u32x4 vt[kCols];
-        const int v0 = v_at(lane);
+        const int v0 = v_col + chunk_at(4 * (lane >> 4) + (lane >> 2 & 3), v_chunk + (lane >> 1 & 1)) + (lane & 1) * 8;
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
           const unsigned char* at = buf + (v0 ^ c * 32);
           const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at));
-          const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + kHalf)));
+          const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 16 * kMain)));
           vt[c] = (u32x4){x[0], x[1], y[0], y[1]};
         }
         if (__ballot(odd) != 0) {
@@ -284,16 +279,16 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
             // up to the one whose window ends with it.
             const int r_from = max(j - (int)s.pos, 0) * Hq - row0;
             const int r_to = a.window > 0 ? (int)min((int64_t)s.n, j - s.pos + a.window) * Hq - row0 : R - row0;
-            const unsigned char* row = buf + at * kRowBytes + wave * 128 + (lane_ >> 4 & 1) * 8;
+            const unsigned char* row = buf + v_col + (lane_ >> 4 & 1) * 8;
 #pragma unroll
             for (int n = 0; n < RB; ++n) {
               const int r = 16 * n + (lane_ & 15);
               const bool sees = r >= r_from && r < r_to;
               __builtin_amdgcn_sched_barrier(0);  // one block's terms at a time: registers
-              const float x = bf16_lo(reinterpret_cast<const uint16_t*>(&lds_p[n][4 * (at & 12) + (lane_ & 15)])[e]);
+              const float x = bf16_lo(reinterpret_cast<const uint16_t*>(&lds_p[i & 1][n][4 * (at & 12) + (lane_ & 15)])[e]);
 #pragma unroll
               for (int c = 0; c < kCols; ++c) {
-                const u32x2 v = *reinterpret_cast<const u32x2*>(row + ((2 * c + (lane_ >> 5)) ^ swizzle(at & 15)) * 16);
+                const u32x2 v = *reinterpret_cast<const u32x2*>(row + chunk_at(at, v_chunk + 2 * c + (lane_ >> 5)));
                 const float y[4] = {bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) out[n][c][k] = sees ? out[n][c][k] + x * y[k] : out[n][c][k];
@@ -303,28 +298,29 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
         }
 #pragma unroll
         for (int n = 0; n < RB; ++n) {
-          const bf16x8 w = __builtin_bit_cast(bf16x8, lds_p[n][lane]);
+          const bf16x8 w = __builtin_bit_cast(bf16x8, lds_p[i & 1][n][lane]);
 #pragma unroll
           for (int c = 0; c < kCols; ++c) out[n][c] = mfma_bf16(__builtin_bit_cast(bf16x8, vt[c]), w, out[n][c]);
         }
       };
 
-      // Tile i is being weighed while tile i + 1 is scored; the buffer that a
-      // new tile goes to was weighed before the last barrier but one.
+      // Tile i is weighed while tile i + 1 is scored; the buffer that a new
+      // tile goes to was weighed before the barrier.
       int issued = -1;
       for (; issued + 1 < min(AHEAD, n_tiles);) load(++issued);
+      // The queries, behind the first tiles' loads.
+      const int q_row = row0 + 16 * wave + (here(lane) & 15);
+      const bf16_t* q_at = static_cast<const bf16_t*>(a.q.p) + (int64_t)(s.row0 + q_row / Hq) * a.q.stride +
+                           q_row % Hq * kDk + 8 * (here(lane) >> 4);
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+        q[k] = wave < RB && q_row < R ? *reinterpret_cast<const bf16x8*>(q_at + 32 * k) : bf16x8{};
       for (int i = -1; i < n_tiles; ++i) {
         if (i + 1 < n_tiles) landed(i + 1, issued);
         lds_barrier();
-        if (i >= 0) {
-          if (i + AHEAD < n_tiles) load(++issued);
-          output(i);
-        }
-        if (i + 1 < n_tiles) {
-          scores(i + 1);
-          lds_barrier();
-          softmax(i + 1);
-        }
+        if (i >= 0 && i + AHEAD < n_tiles) load(++issued);
+        if (i + 1 < n_tiles) scores(i + 1);
+        if (i >= 0) output(i);
       }
 
       // Sums to the rows' own lanes, and out.
@@ -366,8 +362,7 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
       }
       __syncthreads();
     }
-    first += s.tiles;
-    tile = stop;
+    run.next(stop);
   }
 }
 
