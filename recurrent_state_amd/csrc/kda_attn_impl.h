@@ -2,14 +2,20 @@
 // split over the chip, how a wave reaches the pages, and how partial results
 // are joined.
 //
-// Split.  The visible tokens of all sequences, cut into tiles, form one list,
-// and the grid's workers take equal runs of it, whatever the lengths are: a
-// batch of one long and many short sequences keeps every CU busy to the end.
-// The runs follow from the positions on the device, so the host needs no
-// lengths.  A run may hold whole sequences, whose outputs its worker writes
-// itself, and at most two pieces of sequences, which go to the workspace (slot
-// 0: a sequence that an earlier worker began, slot 1: one that a later worker
-// ends) and are joined, in the workers' order, by a second kernel.
+// Split.  The visible tokens of each sequence are cut into tiles, and the grid's
+// workers share the tiles out by the positions on the device, so that the host
+// needs no lengths.
+//   many sequences  All tiles form one list, of which every worker takes an
+//                   equal run: a batch of long and short sequences keeps every
+//                   CU busy to the end.  A run may hold whole sequences, whose
+//                   outputs its worker writes itself, and at most two pieces
+//                   of others.
+//   few (two workers or more to each of up to 64)  Every worker takes a piece
+//                   of one sequence, of the shortest length with which the
+//                   workers suffice: somewhat less even, but a worker loads
+//                   queries and writes results once.
+// Pieces go to the workspace (slot 0: a sequence that an earlier worker began,
+// slot 1: the others) and are joined, in the workers' order, by a second kernel.
 #pragma once
 
 #include "kda_pages.h"
@@ -132,9 +138,7 @@ __device__ __forceinline__ int32_t wave_scan(int32_t x) {
 struct Shares {
   uint32_t count, each, more;
 
-  __device__ __forceinline__ Shares(const AttnArgs& a, uint32_t total) {
-    const uint32_t most = (total + a.run_tiles - 1) / a.run_tiles;
-    count = most < (uint32_t)a.workers ? most : a.workers;
+  __device__ __forceinline__ Shares(uint32_t total, uint32_t count_) : count(count_) {
     each = count ? total / count : 0;
     more = total - each * count;
   }
@@ -168,7 +172,11 @@ struct Run {
       if (record && lanes.err) set_err(a.kb.dev_err, lanes.err);
       total += __builtin_amdgcn_readlane(upto, kWave - 1);
     }
-    const Shares shares(a, total);
+    if (B <= kWave && 2 * B <= a.workers) {
+      one_piece(worker, record, lanes, total);
+      return;
+    }
+    const Shares shares(total, min((total + a.run_tiles - 1) / a.run_tiles, a.workers));
     if (worker < (int)shares.count) {
       tile = shares.begin(worker);
       end = shares.begin(worker + 1);
@@ -204,6 +212,29 @@ struct Run {
     b += at;
     first = before + __builtin_amdgcn_readlane(upto - lanes.tiles, at);
     s = seq_of_lane(lanes, at);
+  }
+
+  // Pieces of single sequences: see the top of the file.
+  __device__ __forceinline__ void one_piece(int worker, bool record, const Seq& lanes, int32_t total) {
+    const int lane = threadIdx.x & 63;
+    const int busy = __popcll(__ballot(lanes.tiles > 0));
+    // Of n pieces of a sequence the last is half empty on average.
+    int32_t each = max(a.run_tiles, (int)((uint32_t)total / (uint32_t)(a.workers - busy / 2)));
+    int32_t count, upto;
+    for (;; each += max(1, each / 16)) {  // ends: from total / (workers - busy) on there are enough
+      count = (lanes.tiles + each - 1) / each;
+      upto = wave_scan(count);
+      if (__builtin_amdgcn_readlane(upto, kWave - 1) <= a.workers) break;
+    }
+    if (record && lane < a.kb.s.B) a.span[lane] = make_int2(upto - count, max(upto - 1, upto - count));
+    const uint64_t past = __ballot(upto > worker);
+    if (past == 0) return;
+    b = __ffsll((unsigned long long)past) - 1;
+    s = seq_of_lane(lanes, b);
+    const Shares shares(s.tiles, __builtin_amdgcn_readlane(count, b));
+    const int piece = worker - __builtin_amdgcn_readlane(upto - count, b);
+    tile = shares.begin(piece);
+    end = shares.begin(piece + 1);
   }
 
   // Sequence `seq`, whose tiles end before tile `upto`.

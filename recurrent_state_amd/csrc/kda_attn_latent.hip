@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
   // Tiles in the LDS: one being scored, one being weighed, the others on
   // their way (what the probabilities leave room for).
   constexpr int BUFS = RB == 8 ? 3 : 4, AHEAD = BUFS - 1;
+  constexpr int kDepth = RB == 8 ? 4 : 12;
   __shared__ __attribute__((aligned(1024))) unsigned char lds[BUFS * kBufBytes];
   __shared__ u32x4 lds_p[2][RB][kWave];        // probabilities, of even and odd tiles
   __shared__ float lds_keep[2][RB][16];        // factors of the sums so far,
@@ -173,16 +174,26 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
         const int t0 = tok0 + i * kTile, lane = here((int)threadIdx.x & 63), g = lane >> 4, row = lane & 15;
         const unsigned char* buf = lds + i % BUFS * kBufBytes;
         f32x4 p[2] = {f32x4{}, f32x4{}};
+        // Key chunk 4 k + g of token group u; kDepth reads are ahead of their
+        // products.  The order is fixed: the compiler's own has every product
+        // wait for its read.
+        auto key = [&](int n) {
+          const int k = n >> 1, u = n & 1;
+          const unsigned char* at =
+              k < 16 ? buf + chunk_at(row, 4 * (k & 3) + g) + (k >> 2) * 256 + u * 16 * kMain
+                     : buf + kTailAt + (16 * u + row) * kTail + ((4 * (k & 1) + g ^ swizzle_tail(row)) << 4);
+          return *reinterpret_cast<const bf16x8*>(at);
+        };
+        bf16x8 keys[kDepth];
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k)
+        for (int n = 0; n < kDepth; ++n) keys[n] = key(n);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            // Key chunk 4 k + g.
-            const unsigned char* at =
-                k < 16 ? buf + chunk_at(row, 4 * (k & 3) + g) + (k >> 2) * 256 + u * 16 * kMain
-                       : buf + kTailAt + (16 * u + row) * kTail + ((4 * (k & 1) + g ^ swizzle_tail(row)) << 4);
-            p[u] = mfma_bf16(*reinterpret_cast<const bf16x8*>(at), q[k], p[u]);
-          }
+        for (int n = 0; n < 2 * kSteps; ++n) {
+          __builtin_amdgcn_sched_barrier(0);
+          p[n & 1] = mfma_bf16(keys[n % kDepth], q[n >> 1], p[n & 1]);
+          if (n + kDepth < 2 * kSteps) keys[n % kDepth] = key(n + kDepth);
+        }
+        __builtin_amdgcn_sched_barrier(0);
         float top = -INFINITY;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -296,11 +307,14 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
             }
           }
         }
+        auto weights = [&](int n) { return __builtin_bit_cast(bf16x8, lds_p[i & 1][n][lane]); };
+        bf16x8 w[2] = {weights(0), weights(1)};
 #pragma unroll
         for (int n = 0; n < RB; ++n) {
-          const bf16x8 w = __builtin_bit_cast(bf16x8, lds_p[i & 1][n][lane]);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) out[n][c] = mfma_bf16(__builtin_bit_cast(bf16x8, vt[c]), w, out[n][c]);
+          for (int c = 0; c < kCols; ++c) out[n][c] = mfma_bf16(__builtin_bit_cast(bf16x8, vt[c]), w[n & 1], out[n][c]);
+          if (n + 2 < RB) w[n & 1] = weights(n + 2);
         }
       };
 
@@ -318,9 +332,14 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
       for (int i = -1; i < n_tiles; ++i) {
         if (i + 1 < n_tiles) landed(i + 1, issued);
         lds_barrier();
-        if (i >= 0 && i + AHEAD < n_tiles) load(++issued);
-        if (i + 1 < n_tiles) scores(i + 1);
-        if (i >= 0) output(i);
+        // Half of the waves (one of each SIMD) begin with the scores, which are
+        // bound by LDS reads, the others with the output, bound by the MFMAs.
+        if (wave < 4 && i + 1 < n_tiles) scores(i + 1);
+        if (i >= 0) {
+          if (i + AHEAD < n_tiles) load(++issued);
+          output(i);
+        }
+        if (wave >= 4 && i + 1 < n_tiles) scores(i + 1);
       }
 
       // Sums to the rows' own lanes, and out.
