@@ -743,12 +743,17 @@ def _need_gpu(t, name):
         raise ValueError(f"{name} is on {t.device}: the library reads device memory")
 
 
+# The current stream's handle without building a torch.cuda.Stream around it (0.1 against 2.7 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch_on(device, fn, args):
     """Calls fn on the current stream of the tensors' device."""
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _launch_on(device, fn, args)
-    _check(fn(*args, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)))
+    _check(fn(*args, _raw_stream(device.index)))
 
 
 def _kv_shape(pool: PagePool, table, pos, Hq, T, in_dtype, tok_start):

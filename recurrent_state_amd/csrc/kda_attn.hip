@@ -490,10 +490,7 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
       const bool complete = tile == first && stop == first + s.tiles;
       const int64_t piece = piece_index(a, worker, tile > first ? 0 : 1, hk, rb);
       const bool bad = __syncthreads_or(walk.bad);
-      if (tid == 0) {
-        if (bad) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
-        if (!complete) a.piece_bad[piece] = bad;
-      }
+      if (bad && tid == 0) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         float total = l[n];
@@ -524,7 +521,7 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
             if (!complete) {
               const int64_t row = piece * a.rows + 16 * n + in;
               store8(a.piece_o + row * D + c0, o);
-              if (c0 == 0) a.piece_ml[row] = (f32x2){M, L};
+              if (c0 == 0) a.piece_ml[row] = (f32x2){M, bad ? -1.f : L};
             } else if (!bad) {
               const float inv = L == 0.f ? 0.f : v_scale / L;
 #pragma unroll

@@ -43,9 +43,9 @@ struct AttnArgs {
   int32_t row_blocks;  // blocks of query rows of a (sequence, kv head)
   int32_t rows;        // query rows of a block
   // Workspace: each sequence's first and last worker [B], then for every piece
-  // (worker, slot, kv head, row block) a flag, (max, sum) and output rows.
+  // (worker, slot, kv head, row block) its rows' (max, sum) and outputs.  A sum
+  // below zero refuses the sequence.
   int2* span;
-  int32_t* piece_bad;
   f32x2* piece_ml;
   float* piece_o;
 };
@@ -122,14 +122,16 @@ __device__ __forceinline__ Seq seq_of_lane(const Seq& x, int from) {
   return s;
 }
 
-// Inclusive sum over the wave's lanes.
+// Inclusive sum over the wave's lanes: inside each 16-lane row by shifts of 1,
+// 2, 4 and 8, then the last lane of a row to the row after it and of the lower
+// half to the upper.  No LDS, no barrier.
 __device__ __forceinline__ int32_t wave_scan(int32_t x) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) {
-    const int32_t y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);   // row_shr:1
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);   // row_shr:2
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);   // row_shr:4
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);   // row_shr:8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2 and 3
   return x;
 }
 
@@ -333,37 +335,57 @@ __global__ void __launch_bounds__(DV / 4 * kJoinGroups<DV>) join_kernel(AttnArgs
   const int share = group & (split - 1), rows_at_once = kJoinGroups<DV> / split;
   const int r0 = blockIdx.z * rows_each, r1 = min(r0 + rows_each, sr.n * G);
   if (r0 >= r1) return;
-  // Refused (every row block of a worker met the same pages): nothing is written.
-  int bad = 0;
-  for (int w = w0 + threadIdx.x; w <= w1; w += blockDim.x)
-    bad |= a.piece_bad[piece_index(a, w, w == w0 ? 1 : 0, hk, r0 / a.rows)];
-  if (__syncthreads_or(bad)) return;
   const float vs = kb.pages.v_scale ? kb.pages.v_scale[hk] : 1.f;
   for (int rr = r0; rr < r1; rr += rows_at_once) {
     const bool live = rr + group / split < r1;
     const int r = live ? rr + group / split : r0;
     const int rb = r / a.rows, in = r % a.rows;
     const auto row_of = [&](int w) { return piece_index(a, w, w == w0 ? 1 : 0, hk, rb) * a.rows + in; };
-    float m = -INFINITY, l = 0.f;
-    for (int w = w0 + same; w <= w1; w += SAME) m = fmaxf(m, a.piece_ml[row_of(w)][0]);
+    // The first pieces' outputs are asked for before their weights are known.
+    constexpr int FIRST = 4;
+    f32x4 x[FIRST];
+    float xm[FIRST];
+#pragma unroll
+    for (int j = 0; j < FIRST; ++j) {
+      const int w = w0 + share + j * split;
+      const int64_t row = row_of(min(w, w1));
+      x[j] = *reinterpret_cast<const f32x4*>(a.piece_o + row * DV + 4 * lane);
+      xm[j] = w <= w1 ? a.piece_ml[row][0] : -INFINITY;
+    }
+    const f32x2 none = {-INFINITY, 0.f};
+    const f32x2 ml = w0 + same <= w1 ? a.piece_ml[row_of(w0 + same)] : none;
+    float m = ml[0];
+    int refused = ml[1] < 0.f;
+    for (int w = w0 + same + SAME; w <= w1; w += SAME) {
+      const f32x2 y = a.piece_ml[row_of(w)];
+      m = fmaxf(m, y[0]);
+      refused |= y[1] < 0.f;
+    }
+    // Every row of the sequence comes out the same, so the workgroup agrees.
+    if (__ballot(refused) != 0) return;
 #pragma unroll
     for (int d = 1; d < SAME; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
     // A piece in which the row sees no token has m = -inf and zeros.
     const float top = m == -INFINITY ? 0.f : m;
-    for (int w = w0 + same; w <= w1; w += SAME) {
-      const f32x2 ml = a.piece_ml[row_of(w)];
-      l += ml[1] * exp2_(ml[0] - top);
+    float l = ml[1] * exp2_(ml[0] - top);
+    for (int w = w0 + same + SAME; w <= w1; w += SAME) {
+      const f32x2 y = a.piece_ml[row_of(w)];
+      l += y[1] * exp2_(y[0] - top);
     }
 #pragma unroll
     for (int d = 1; d < SAME; d *= 2) l += __shfl_xor(l, d);
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < FIRST; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] += w0 + share + j * split <= w1 ? x[j][i] * exp2_(xm[j] - top) : 0.f;
 #pragma unroll 4
-    for (int w = w0 + share; w <= w1; w += split) {
+    for (int w = w0 + share + FIRST * split; w <= w1; w += split) {
       const int64_t row = row_of(w);
       const float f = exp2_(a.piece_ml[row][0] - top);
-      const f32x4 x = *reinterpret_cast<const f32x4*>(a.piece_o + row * DV + 4 * lane);
+      const f32x4 y = *reinterpret_cast<const f32x4*>(a.piece_o + row * DV + 4 * lane);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] += x[i] * f;
+      for (int i = 0; i < 4; ++i) o[i] += y[i] * f;
     }
     if (split > 1) {
       part[group][lane] = o;
@@ -402,13 +424,12 @@ inline int workers_of(const kda_kv_shape& s, int64_t wgs, const Split& d, int32_
 }
 
 struct Workspace {
-  size_t bad, ml, o, total;
+  size_t ml, o, total;
 };
 inline Workspace workspace_of(const kda_kv_shape& s, const Split& d) {
   const size_t pieces = (size_t)d.workers * 2 * s.Hkv * d.row_blocks;
   Workspace L;
-  L.bad = round_up((size_t)s.B * 8, 256);
-  L.ml = round_up(L.bad + pieces * 4, 256);
+  L.ml = round_up((size_t)s.B * 8, 256);
   L.o = round_up(L.ml + pieces * d.rows * 8, 256);
   L.total = round_up(L.o + pieces * d.rows * s.dv * 4, 256);
   return L;
@@ -423,8 +444,7 @@ inline AttnArgs make_args(const KvBatch& b, KvRows q, float scale, int32_t windo
                   o,         lse,
                   d.workers, d.run_tiles, d.row_blocks,
                   d.rows,    reinterpret_cast<int2*>(ws),
-                  reinterpret_cast<int32_t*>(ws + L.bad), reinterpret_cast<f32x2*>(ws + L.ml),
-                  reinterpret_cast<float*>(ws + L.o)};
+                  reinterpret_cast<f32x2*>(ws + L.ml), reinterpret_cast<float*>(ws + L.o)};
 }
 
 // The join after an attention kernel.  A sequence has about workers / B pieces

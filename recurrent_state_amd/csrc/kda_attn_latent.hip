@@ -346,10 +346,7 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
       const bool complete = tile == first && stop == first + s.tiles;
       const int64_t piece = piece_index(a, worker, tile > first ? 0 : 1, 0, rb);
       const bool bad = __syncthreads_or(walk.bad);
-      if (threadIdx.x == 0) {
-        if (bad) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
-        if (!complete) a.piece_bad[piece] = bad;
-      }
+      if (bad && threadIdx.x == 0) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
       if (wave < RB) {
         const float sum = pair_sum32(pair_sum16(l));
         if (lane < 16) lds_ml[wave][lane] = (f32x2){m, sum};
@@ -365,7 +362,7 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
           const int64_t row = piece * a.rows + in;
 #pragma unroll
           for (int c = 0; c < kCols; ++c) store4(a.piece_o + row * kDv + c0 + 16 * c, out[n][c]);
-          if (c0 == 0) a.piece_ml[row] = ml;
+          if (c0 == 0) a.piece_ml[row] = (f32x2){ml[0], bad ? -1.f : ml[1]};
         } else if (!bad) {
           const float inv = ml[1] == 0.f ? 0.f : 1.f / ml[1];
           const int64_t row = (int64_t)(s.row0 + r / Hq) * Hq + r % Hq;
