@@ -75,16 +75,24 @@ struct Weights {
   }
 };
 
+template <bool NT, typename V, typename T>
+__device__ __forceinline__ V load(const T* p) {
+  const V* v = reinterpret_cast<const V*>(p);
+  return NT ? __builtin_nontemporal_load(v) : *v;
+}
+
 // One wave's share of the keys and values of SUB tokens, in the layout that
 // the loads give, and the operands made from it.  Token t of the share is row
 // `t & 15` of group `t >> 4`; pk / pv point to each group's first row.
 //
+// NT: loads that leave the caches to others (see run()).
+//
 // bf16: 32 tokens, 32 contraction slots.
-template <int D, typename TC>
+template <int D, typename TC, bool NT>
 struct Cache;
 
-template <int D>
-struct Cache<D, bf16_t> {
+template <int D, bool NT>
+struct Cache<D, bf16_t, NT> {
   static constexpr int GROUPS = 2, SUB = 32;
   static constexpr int VC = D / 16;  // neighbouring values of a row in a lane
   u32x4 k[2][D / 32];
@@ -103,7 +111,7 @@ struct Cache<D, bf16_t> {
     const int l = threadIdx.x & 63;
 #pragma unroll
     for (int s = 0; s < D / 32; ++s)
-      k[u][s] = *reinterpret_cast<const u32x4*>(rows + (l & 15) * D + 32 * s + 8 * (l >> 4));
+      k[u][s] = load<NT, u32x4>(rows + (l & 15) * D + 32 * s + 8 * (l >> 4));
   }
   __device__ __forceinline__ void load_v(int u, const bf16_t* rows) {
     const int l = threadIdx.x & 63;
@@ -111,11 +119,11 @@ struct Cache<D, bf16_t> {
     for (int j = 0; j < 4; ++j) {
       const bf16_t* p = rows + (4 * (l >> 4) + j) * D + VC * (l & 15);
       if constexpr (VC == 8) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+        const u32x4 w = load<NT, u32x4>(p);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[4 * u + j][i] = w[i];
       } else {
-        const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+        const u32x2 w = load<NT, u32x2>(p);
         v[4 * u + j][0] = w[0];
         v[4 * u + j][1] = w[1];
       }
@@ -160,8 +168,8 @@ struct Cache<D, bf16_t> {
 
 // e4m3: as bf16, widened when used.  A key load of 16 bytes feeds two
 // contraction steps, so the queries are laid out to match.
-template <int D>
-struct Cache<D, uint8_t> {
+template <int D, bool NT>
+struct Cache<D, uint8_t, NT> {
   static constexpr int GROUPS = 2, SUB = 32;
   static constexpr int VC = D / 16;
   u32x4 k[2][D / 64];
@@ -180,7 +188,7 @@ struct Cache<D, uint8_t> {
     const int l = threadIdx.x & 63;
 #pragma unroll
     for (int s = 0; s < D / 64; ++s)
-      k[u][s] = *reinterpret_cast<const u32x4*>(rows + (l & 15) * D + 64 * s + 16 * (l >> 4));
+      k[u][s] = load<NT, u32x4>(rows + (l & 15) * D + 64 * s + 16 * (l >> 4));
   }
   __device__ __forceinline__ void load_v(int u, const uint8_t* rows) {
     const int l = threadIdx.x & 63;
@@ -188,11 +196,11 @@ struct Cache<D, uint8_t> {
     for (int j = 0; j < 4; ++j) {
       const uint8_t* p = rows + (4 * (l >> 4) + j) * D + VC * (l & 15);
       if constexpr (VC == 8) {
-        const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+        const u32x2 w = load<NT, u32x2>(p);
         v[4 * u + j][0] = w[0];
         v[4 * u + j][1] = w[1];
       } else {
-        v[4 * u + j][0] = *reinterpret_cast<const uint32_t*>(p);
+        v[4 * u + j][0] = load<NT, uint32_t>(p);
       }
     }
   }
@@ -233,8 +241,8 @@ struct Cache<D, uint8_t> {
 
 // fp32: 16 tokens; a contraction step takes four k-slots, one to each lane
 // group.  V^T tile (64 h + c): columns 64 h + 4 m + c.
-template <int D>
-struct Cache<D, float> {
+template <int D, bool NT>
+struct Cache<D, float, NT> {
   static constexpr int GROUPS = 1, SUB = 16;
   static constexpr int VC = D / 16;
   f32x4 k[1][D / 16];
@@ -253,7 +261,7 @@ struct Cache<D, float> {
     const int l = threadIdx.x & 63;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s)
-      k[u][s] = *reinterpret_cast<const f32x4*>(rows + (l & 15) * D + 16 * s + 4 * (l >> 4));
+      k[u][s] = load<NT, f32x4>(rows + (l & 15) * D + 16 * s + 4 * (l >> 4));
   }
   __device__ __forceinline__ void load_v(int, const float* rows) {
     const int l = threadIdx.x & 63;
@@ -261,7 +269,7 @@ struct Cache<D, float> {
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int h = 0; h < D / 64; ++h)
-        v[j][h] = *reinterpret_cast<const f32x4*>(rows + (4 * (l >> 4) + j) * D + 64 * h + 4 * (l & 15));
+        v[j][h] = load<NT, f32x4>(rows + (4 * (l >> 4) + j) * D + 64 * h + 4 * (l & 15));
   }
   __device__ __forceinline__ f32x4 score(int u, const Query& q) const {
     f32x4 c = {0.f, 0.f, 0.f, 0.f};
@@ -308,9 +316,9 @@ __device__ __forceinline__ int out_col(int g, int c, int i) {
 }
 
 // NQ blocks of 16 query rows to a workgroup.
-template <int D, typename TIn, typename TC, int NQ>
+template <int D, typename TIn, typename TC, int NQ, bool NT>
 __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1) attn_kernel(AttnArgs a) {
-  typedef Cache<D, TC> C;
+  typedef Cache<D, TC, NT> C;
   constexpr int SUB = C::SUB, GROUPS = C::GROUPS, VC = C::VC, TILE = kWaves * SUB;
   constexpr int RS = D + 4;  // LDS row stride in floats
   __shared__ float lds_o[kWaves][16][RS];
@@ -557,10 +565,18 @@ Split split_of(const kda_kv_shape& s, int32_t page_size, int32_t max_pages) {
   return d;
 }
 
+// A pool that the 256 MB Infinity Cache cannot hold is read past it with
+// non-temporal loads: 105.8 -> 93.2 us at one sequence of 131071 tokens, 96 ->
+// 88 at 64 of up to 8191, 116 -> 107 in e4m3.  A smaller one may still be there
+// from the call before, and is then read from there: 25 us with plain loads
+// against 29 for 16 sequences whose three pools of 78 MB took turns.
 template <int D, typename TIn, typename TC, int NQ>
 hipError_t run(const AttnArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((attn_kernel<D, TIn, TC, NQ>), dim3(a.workers, a.kb.s.Hkv, a.row_blocks), dim3(kWaves * kWave), 0,
-                     st, a);
+  const dim3 grid(a.workers, a.kb.s.Hkv, a.row_blocks), block(kWaves * kWave);
+  if (outgrows_cache(a.kb))
+    hipLaunchKernelGGL((attn_kernel<D, TIn, TC, NQ, true>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((attn_kernel<D, TIn, TC, NQ, false>), grid, block, 0, st, a);
   const hipError_t e = hipGetLastError();
   return e != hipSuccess ? e : run_join<D, TIn>(a, st);
 }

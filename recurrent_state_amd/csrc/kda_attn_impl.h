@@ -408,6 +408,13 @@ __global__ void __launch_bounds__(DV / 4 * kJoinGroups<DV>) join_kernel(AttnArgs
   }
 }
 
+// Whether the pool is larger than the 256 MB that the memory side caches.
+inline bool outgrows_cache(const KvBatch& kb) {
+  const int64_t es = kb.s.cache_dtype == KDA_F32 ? 4 : kb.s.cache_dtype == KDA_BF16 ? 2 : 1;
+  const int64_t row = kb.pages.v ? kb.s.dk + kb.s.dv : kb.s.dk;
+  return ((int64_t)kb.pages.n_pages * kb.s.Hkv << kb.page_shift) * row * es > (int64_t)256 << 20;
+}
+
 // How a call is split: see split_of() of each kernel.
 struct Split {
   int tile, rows, row_blocks, workers, run_tiles;
