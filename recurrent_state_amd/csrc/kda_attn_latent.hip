@@ -12,10 +12,11 @@
 //            whose queries it holds (72 registers): the rows' maxima and sums
 //            stay in its registers, and the probabilities go to the LDS as an
 //            MFMA operand.
-//   output   O^T += V^T P^T.  Every wave has 64 of the 512 columns of all rows
-//            (32 to 128 registers), so a value is read from the LDS once.  V^T
-//            comes from ds_read_b64_tr_b16, which hands lane l column l & 15
-//            of four rows.
+//   output   O^T += V^T P^T.  A wave has 64 of the 512 columns of all rows, or
+//            128 where the other four waves make the scores (up to 64 rows; 64
+//            or 128 registers), so a value is read from the LDS once.  V^T comes
+//            from ds_read_b64_tr_b16, which hands lane l column l & 15 of four
+//            rows.
 //
 // Between two barriers the waves score tile i + 1 and weigh tile i, while later
 // tiles are on their way (LDS-direct loads, 16 bytes a lane).  So the two waves
@@ -46,7 +47,6 @@ constexpr int kRowBytes = kDk * 2;          // in the pages: 72 chunks of 16 byt
 constexpr int kMain = kDv * 2, kTail = kRowBytes - kMain;  // in the LDS: see above
 constexpr int kTailAt = kTile * kMain, kBufBytes = kTile * kRowBytes;
 constexpr int kSteps = kDk / 32;            // contraction steps
-constexpr int kCols = kDv / kWaves / 16;    // column tiles of a wave
 
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -75,6 +75,8 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
   // their way (what the probabilities leave room for).
   constexpr int BUFS = RB == 8 ? 3 : 4, AHEAD = BUFS - 1;
   constexpr int kDepth = RB == 8 ? 4 : 12;
+  constexpr int OUT = RB == 8 ? 8 : 4;      // waves that make the output: the last ones
+  constexpr int kCols = kDv / OUT / 16;     // column tiles of such a wave
   __shared__ __attribute__((aligned(1024))) unsigned char lds[BUFS * kBufBytes];
   __shared__ u32x4 lds_p[2][RB][kWave];        // probabilities, of even and odd tiles
   __shared__ float lds_keep[2][RB][16];        // factors of the sums so far,
@@ -87,23 +89,25 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
   Run<kTile> run(a, worker, worker == 0 && rb == 0 && wave == 0);
   const float x_scale = a.scale * kLog2e;
 
-  // Byte offset in a tile of chunk c (below 16) of row `row`, for this wave's
-  // columns the chunks 8 (wave & 1) and on after chunk 16 (wave / 2).  Lane
-  // constants are computed where they are used (here()): registers are short.
+  // Byte offset in a tile of chunk c (below 16) of row `row`; this wave's
+  // columns begin at chunk v_chunk after v_col bytes.  Lane constants are
+  // computed where they are used (here()): registers are short.
   auto chunk_at = [](int row, int c) { return row * kMain + ((c ^ swizzle(row & 15)) << 4); };
-  const int v_col = (wave >> 1) * 256, v_chunk = 8 * (wave & 1);
+  const int ow = wave - (kWaves - OUT);
+  const int v_col = (OUT == 8 ? ow >> 1 : ow) * 256, v_chunk = OUT == 8 ? 8 * (ow & 1) : 0;
 
   while (run.tile < run.end) {
     const Seq& s = run.s;
     const int32_t tile = run.tile, first = run.first, stop = min(run.end, first + s.tiles);
     const int R = s.n * Hq, row0 = rb * RB * 16;
     if (row0 < R) {
-      bf16x8 q[kSteps];
-      f32x4 out[RB][kCols];
+      // The outputs [row block][column tile], and the queries: after them where a
+      // wave holds both, else in the same registers.
+      constexpr int Q0 = OUT == kWaves ? RB * kCols : 0;
+      constexpr int HELD = RB * kCols > Q0 + kSteps ? RB * kCols : Q0 + kSteps;
+      f32x4 held[HELD];
 #pragma unroll
-      for (int n = 0; n < RB; ++n)
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) out[n][c] = f32x4{};
+      for (int x = 0; x < HELD; ++x) held[x] = f32x4{};
       float m = -INFINITY, l = 0.f;  // of the rows that the wave scores
       const int my_row = row0 + 16 * wave + (here(lane) & 15);
       const int vis = my_row < R ? (int)max(s.pos + my_row / Hq, (int64_t)-1) : -1;  // the last token it sees
@@ -190,7 +194,7 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
 #pragma unroll
         for (int n = 0; n < 2 * kSteps; ++n) {
           __builtin_amdgcn_sched_barrier(0);
-          p[n & 1] = mfma_bf16(keys[n % kDepth], q[n >> 1], p[n & 1]);
+          p[n & 1] = mfma_bf16(keys[n % kDepth], __builtin_bit_cast(bf16x8, held[Q0 + (n >> 1)]), p[n & 1]);
           if (n + kDepth < 2 * kSteps) keys[n % kDepth] = key(n + kDepth);
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -236,6 +240,7 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
       };
 
       auto output = [&](int i) {
+        if (OUT < kWaves && ow < 0) return;
         const int t0 = tok0 + i * kTile, lane = here((int)threadIdx.x & 63);
         const unsigned char* buf = lds + i % BUFS * kBufBytes;
         const uint64_t grown = __ballot(lane < RB && lds_grown[i & 1][lane % RB] != 0);
@@ -247,7 +252,7 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
 #pragma unroll
               for (int c = 0; c < kCols; ++c)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) out[n][c][j] *= keep;
+                for (int j = 0; j < 4; ++j) held[n * kCols + c][j] *= keep;
             }
         }
         // A probability of zero must meet a finite value: look at the tokens
@@ -255,9 +260,10 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
         bool odd = false;
         if (!whole(t0)) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int j = t0 + 8 * x + (lane >> 3);
-            const u32x4 v = *reinterpret_cast<const u32x4*>(buf + v_col + chunk_at(j - t0, v_chunk + (lane & 7)));
+          for (int x = 0; x < kCols; ++x) {
+            const int c = x * kWave + lane, j = t0 + c / (2 * kCols);
+            const u32x4 v =
+                *reinterpret_cast<const u32x4*>(buf + v_col + chunk_at(j - t0, v_chunk + c % (2 * kCols)));
             uint32_t peak = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) peak = max(peak, max(v[e] << 16 & 0x7fff0000u, v[e] & 0x7fff0000u));
@@ -302,7 +308,10 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
                 const u32x2 v = *reinterpret_cast<const u32x2*>(row + chunk_at(at, v_chunk + 2 * c + (lane_ >> 5)));
                 const float y[4] = {bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) out[n][c][k] = sees ? out[n][c][k] + x * y[k] : out[n][c][k];
+                for (int k = 0; k < 4; ++k) {
+                  const float o = held[n * kCols + c][k];
+                  held[n * kCols + c][k] = sees ? o + x * y[k] : o;
+                }
               }
             }
           }
@@ -313,7 +322,8 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
         for (int n = 0; n < RB; ++n) {
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) out[n][c] = mfma_bf16(__builtin_bit_cast(bf16x8, vt[c]), w[n & 1], out[n][c]);
+          for (int c = 0; c < kCols; ++c)
+            held[n * kCols + c] = mfma_bf16(__builtin_bit_cast(bf16x8, vt[c]), w[n & 1], held[n * kCols + c]);
           if (n + 2 < RB) w[n & 1] = weights(n + 2);
         }
       };
@@ -326,14 +336,16 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
       const int q_row = row0 + 16 * wave + (here(lane) & 15);
       const bf16_t* q_at = static_cast<const bf16_t*>(a.q.p) + (int64_t)(s.row0 + q_row / Hq) * a.q.stride +
                            q_row % Hq * kDk + 8 * (here(lane) >> 4);
+      if (wave < RB && q_row < R) {
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k)
-        q[k] = wave < RB && q_row < R ? *reinterpret_cast<const bf16x8*>(q_at + 32 * k) : bf16x8{};
+        for (int k = 0; k < kSteps; ++k) held[Q0 + k] = *reinterpret_cast<const f32x4*>(q_at + 32 * k);
+      }
       for (int i = -1; i < n_tiles; ++i) {
         if (i + 1 < n_tiles) landed(i + 1, issued);
         lds_barrier();
-        // Half of the waves (one of each SIMD) begin with the scores, which are
-        // bound by LDS reads, the others with the output, bound by the MFMAs.
+        // With 128 rows every wave does both: half of them (one of each SIMD)
+        // begin with the scores, which are bound by LDS reads, the others with
+        // the output, bound by the MFMAs.
         if (wave < 4 && i + 1 < n_tiles) scores(i + 1);
         if (i >= 0) {
           if (i + AHEAD < n_tiles) load(++issued);
@@ -352,23 +364,23 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
         if (lane < 16) lds_ml[wave][lane] = (f32x2){m, sum};
       }
       __syncthreads();
-      const int c0 = wave * (16 * kCols) + 4 * (here(lane) >> 4);
+      const int c0 = ow * (16 * kCols) + 4 * (here(lane) >> 4);
 #pragma unroll
       for (int n = 0; n < RB; ++n) {
         const int in = 16 * n + (here(lane) & 15), r = row0 + in;
-        if (r >= R) continue;
+        if (r >= R || ow < 0) continue;
         const f32x2 ml = lds_ml[n][in & 15];
         if (!complete) {
           const int64_t row = piece * a.rows + in;
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) store4(a.piece_o + row * kDv + c0 + 16 * c, out[n][c]);
+          for (int c = 0; c < kCols; ++c) store4(a.piece_o + row * kDv + c0 + 16 * c, held[n * kCols + c]);
           if (c0 == 0) a.piece_ml[row] = (f32x2){ml[0], bad ? -1.f : ml[1]};
         } else if (!bad) {
           const float inv = ml[1] == 0.f ? 0.f : 1.f / ml[1];
           const int64_t row = (int64_t)(s.row0 + r / Hq) * Hq + r % Hq;
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
-            f32x4 x = out[n][c];
+            f32x4 x = held[n * kCols + c];
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[k] *= inv;
             store4(static_cast<bf16_t*>(a.o) + row * kDv + c0 + 16 * c, x);
@@ -376,7 +388,7 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
           if (a.lse && c0 == 0) a.lse[row] = (ml[0] + __log2f(ml[1])) * kLn2;
         }
       }
-      __syncthreads();
+      lds_barrier();
     }
     run.next(stop);
   }
