@@ -310,15 +310,16 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
 // Joins the pieces of the sequences that more than one worker had a part of:
 // with m the largest of the pieces' maxima,
 //   o = sum_w 2^(m_w - m) o_w / sum_w 2^(m_w - m) l_w.
-// DV / 4 lanes hold a row of outputs, and a workgroup has four to sixteen such
-// groups.
+// DV / 4 lanes hold a row of outputs, and a workgroup has several such groups.
 // `split` of them (a power of two) share a row, each with every split-th
 // piece, so that a long sequence's many pieces are read side by side, and a
 // batch's few pieces of many rows are too; a workgroup takes `rows_each` query
 // rows of a (sequence, kv head).  Every wave finds m and the sum by itself, a
 // piece to a lane.
 template <int DV>
-constexpr int kJoinGroups = DV == 512 ? 4 : DV == 128 ? 8 : 16;
+constexpr int kJoinFirst = DV == 512 ? 8 : 4;  // pieces of a row that a group asks for at once
+template <int DV>
+constexpr int kJoinGroups = DV == 512 ? 8 : 16;  // of a workgroup, at most
 
 template <int DV, typename TIn>
 __global__ void __launch_bounds__(DV / 4 * kJoinGroups<DV>) join_kernel(AttnArgs a, int rows_each, int split) {
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(DV / 4 * kJoinGroups<DV>) join_kernel(AttnArgs
   const SeqRows sr = seq_rows(kb, b);
   constexpr int SAME = LANES < kWave ? LANES : kWave;  // lanes of a wave that hold one row
   const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES, same = threadIdx.x % SAME;
-  const int share = group & (split - 1), rows_at_once = kJoinGroups<DV> / split;
+  const int share = group & (split - 1), rows_at_once = blockDim.x / LANES / split;
   const int r0 = blockIdx.z * rows_each, r1 = min(r0 + rows_each, sr.n * G);
   if (r0 >= r1) return;
   const float vs = kb.pages.v_scale ? kb.pages.v_scale[hk] : 1.f;
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(DV / 4 * kJoinGroups<DV>) join_kernel(AttnArgs
     const int rb = r / a.rows, in = r % a.rows;
     const auto row_of = [&](int w) { return piece_index(a, w, w == w0 ? 1 : 0, hk, rb) * a.rows + in; };
     // The first pieces' outputs are asked for before their weights are known.
-    constexpr int FIRST = 4;
+    constexpr int FIRST = kJoinFirst<DV>;
     f32x4 x[FIRST];
     float xm[FIRST];
 #pragma unroll
@@ -455,20 +456,22 @@ inline AttnArgs make_args(const KvBatch& b, KvRows q, float scale, int32_t windo
 }
 
 // The join after an attention kernel.  A sequence has about workers / B pieces
-// (the lengths are not known here): a row's groups of lanes are at most half as
-// many, and a workgroup takes rows enough that about 2048 of them cover all.
+// (the lengths are not known here): enough groups share a row to ask for all of
+// them at once, and a workgroup takes rows enough that about 2048 of them cover
+// all.
 template <int DV, typename TIn>
 hipError_t run_join(const AttnArgs& a, hipStream_t st) {
   if (a.workers == 1) return hipSuccess;
   const kda_kv_shape& s = a.kb.s;
   const int rows = s.T * (s.Hq / s.Hkv);
-  int split = kJoinGroups<DV>;
-  while (split > 1 && (int64_t)split * 2 * s.B > a.workers) split /= 2;
-  const int at_once = kJoinGroups<DV> / split;
+  int split = 1;
+  while (split < kJoinGroups<DV> && a.workers > (int64_t)split * kJoinFirst<DV> * s.B) split *= 2;
+  const int groups = split > 1024 / DV ? split : 1024 / DV;  // 256 threads or more
+  const int at_once = groups / split;
   int64_t each = ((int64_t)s.B * s.Hkv * rows + 2047) / 2048;
   each = (each + at_once - 1) / at_once * at_once;
   hipLaunchKernelGGL((join_kernel<DV, TIn>), dim3(s.B, s.Hkv, (unsigned)((rows + each - 1) / each)),
-                     dim3(DV / 4 * kJoinGroups<DV>), 0, st, a, (int)each, split);
+                     dim3(DV / 4 * groups), 0, st, a, (int)each, split);
   return hipGetLastError();
 }
 
