@@ -8,6 +8,10 @@
 // rotated), so nothing is exchanged between lanes and q_out may be q itself.
 // A token's units are numbered queries, keys, values; consecutive threads take
 // consecutive units, so a wave covers whole 128-byte lines of a head row.
+//
+// Bound by memory for prompts, and by the chain of dependent loads (token range,
+// position, page) for a few tokens: the unit's values depend on none of these
+// and are asked for first.
 
 #include "kda_pages.h"
 
@@ -25,31 +29,54 @@ struct AppendArgs {
   int32_t units_q, units_k, units;  // units of a token: queries; and keys; and values
 };
 
-// 8 values as fp32.
-__device__ __forceinline__ void load8(const bf16_t* p, float (&x)[8]) {
-  Raw<bf16_t, 8> r;
-  load_raw(p, r);
-  widen(r, x);
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  Raw<float, 8> r;
-  load_raw(p, r);
-  widen(r, x);
-}
-
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 typedef __attribute__((ext_vector_type(2))) float f32x2;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
 
+// NT: non-temporal, for calls that outgrow the caches (see run()).
+template <bool NT, typename V>
+__device__ __forceinline__ V get(const V* p) {
+  return NT ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool NT, typename V>
+__device__ __forceinline__ void put(V* p, const V& x) {
+  if (NT)
+    __builtin_nontemporal_store(x, p);
+  else
+    *p = x;
+}
+
+// 8 values as fp32, and back.
+template <bool NT>
+__device__ __forceinline__ void load8(const bf16_t* p, float (&x)[8]) {
+  const u32x4 w = get<NT>(reinterpret_cast<const u32x4*>(p));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_lo(w[i]);
+    x[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+template <bool NT>
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f32x4 w = get<NT>(reinterpret_cast<const f32x4*>(p) + h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[4 * h + i] = w[i];
+  }
+}
+template <bool NT>
 __device__ __forceinline__ void store8(bf16_t* p, const float (&x)[8]) {
-  uint32_t w[4];
+  u32x4 w;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x[2 * i], x[2 * i + 1]}, bf16x2));
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  put<NT>(reinterpret_cast<u32x4*>(p), w);
 }
+template <bool NT>
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  put<NT>(reinterpret_cast<f32x4*>(p), (f32x4){x[0], x[1], x[2], x[3]});
+  put<NT>(reinterpret_cast<f32x4*>(p) + 1, (f32x4){x[4], x[5], x[6], x[7]});
 }
 
 // e4m3 of x / scale: clamped to the type's largest value (it has no infinity),
@@ -59,6 +86,7 @@ __device__ __forceinline__ float to_range(float x, float scale) {
   const float y = x / scale;
   return y != y ? y : fminf(fmaxf(y, -448.f), 448.f);
 }
+template <bool NT>
 __device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&x)[8], float scale) {
   int w[2] = {0, 0};
 #pragma unroll
@@ -66,7 +94,7 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&x)[8], flo
     w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(to_range(x[4 * i], scale), to_range(x[4 * i + 1], scale), w[i], false);
     w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(to_range(x[4 * i + 2], scale), to_range(x[4 * i + 3], scale), w[i], true);
   }
-  *reinterpret_cast<int2*>(p) = make_int2(w[0], w[1]);
+  put<NT>(reinterpret_cast<u32x2*>(p), (u32x2){(uint32_t)w[0], (uint32_t)w[1]});
 }
 
 // The sequence of packed row `row`: the last one that starts at or before it.
@@ -87,7 +115,7 @@ __device__ __forceinline__ int seq_of_row(const KvBatch& kb, int row) {
   return b;
 }
 
-template <int DK, int DV, typename TIn, typename TC>
+template <int DK, int DV, typename TIn, typename TC, bool NT>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
   constexpr bool kE4m3 = sizeof(TC) == 1;
   const KvBatch& kb = a.kb;
@@ -97,76 +125,82 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
     for (int b = threadIdx.x; b < kb.s.B; b += kThreads)
       if (seq_rows(kb, b).bad) set_err(kb.dev_err, KDA_DEV_ERR_TOKENS);
 
-  const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  // Row and unit of this thread; the threads past the last unit take part in
+  // seq_of_row with that one's row.
   const int64_t total = (int64_t)kb.n_tokens * a.units;
-  const bool live = e < total;  // the whole wave takes part in seq_of_row
-  const int row = (int)((live ? e : total - 1) / a.units);
-  int u = (int)(e - (int64_t)row * a.units);
+  int row, u;
+  bool live = true;
+  if (total <= (int64_t)1 << 31) {
+    const uint32_t e = blockIdx.x * kThreads + threadIdx.x;
+    live = e < (uint32_t)total;
+    const uint32_t at = live ? e : (uint32_t)total - 1;
+    row = (int)(at / (uint32_t)a.units);
+    u = (int)(at - (uint32_t)row * (uint32_t)a.units);
+  } else {
+    const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    live = e < total;
+    const int64_t at = live ? e : total - 1;
+    row = (int)(at / a.units);
+    u = (int)(at - (int64_t)row * a.units);
+  }
+
+  // What the unit is, and its two chunks: rotated units of a head come first.
+  const bool is_value = u >= a.units_k, is_key = !is_value && u >= a.units_q;
+  const bool rotates = a.rot.cos_sin != nullptr;
+  const int n_rot = rotates ? a.rot.dim >> 4 : 0;
+  int h, w = 0, c0, c1;
+  const TIn* src;
+  if (is_value) {
+    const int at = u - a.units_k;
+    h = at / (DV / 16);
+    c0 = at % (DV / 16) * 16;
+    c1 = c0 + 8;
+    src = static_cast<const TIn*>(a.v.p) + row * a.v.stride + h * DV;
+  } else {
+    const int at = is_key ? u - a.units_q : u;
+    h = at / (DK / 16);
+    w = at % (DK / 16);
+    if (w < n_rot) {
+      c0 = a.rot.start + (a.rot.pairs ? 16 * w : 8 * w);
+      c1 = c0 + (a.rot.pairs ? 8 : a.rot.dim >> 1);
+    } else {
+      c0 = 16 * (w - n_rot);
+      if (rotates && c0 >= a.rot.start) c0 += a.rot.dim;
+      c1 = c0 + 8;
+    }
+    src = is_key ? static_cast<const TIn*>(a.k.p) + row * a.k.stride + h * DK
+                 : static_cast<const TIn*>(a.q.p) + row * a.q.stride + h * DK;
+  }
+  float x[8], y[8];
+  load8<NT>(src + c0, x);
+  load8<NT>(src + c1, y);
+
   const int b = kb.tok_start ? seq_of_row(kb, row) : row / kb.s.T;
   if (!live || b < 0) return;
+  const int64_t pos = kb.pos[b];
   const SeqRows sr = seq_rows(kb, b);
   const int i = row - sr.row0;
   if (sr.bad || i < 0 || i >= sr.n) return;
-
-  const int64_t p = kb.pos[b] + i;
-  const bool rotates = a.rot.cos_sin != nullptr;
+  const int64_t p = pos + i;
   if (p < 0 || (rotates && p >= a.rot.max_pos)) {
     if (u == 0) set_err(kb.dev_err, KDA_DEV_ERR_POS);
     return;
   }
   const int64_t at = p >> kb.page_shift;
   const int32_t page = at < kb.max_pages ? kb.table[(int64_t)b * kb.max_pages + at] : -1;
+  float cc[8], ss[8];
+  const bool turn = !is_value && w < n_rot;
+  if (turn) {
+    const float* cs = a.rot.cos_sin + p * a.rot.dim + 8 * w;
+    load8<false>(cs, cc);
+    load8<false>(cs + (a.rot.dim >> 1), ss);
+  }
   if (page < 0 || page >= kb.pages.n_pages) {
     if (u == 0) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
     return;
   }
-  const int slot = (int)p & (kb.pages.page_size - 1);
 
-  if (u >= a.units_k) {  // a value: stored as it is
-    u -= a.units_k;
-    const int h = u / (DV / 16), c = u % (DV / 16) * 16;
-    const TIn* src = static_cast<const TIn*>(a.v.p) + row * a.v.stride + h * DV + c;
-    TC* dst = static_cast<TC*>(kb.pages.v) +
-              ((((int64_t)page * kb.s.Hkv + h) << kb.page_shift) + slot) * DV + c;
-    float x[8], y[8];
-    load8(src, x);
-    load8(src + 8, y);
-    if constexpr (kE4m3) {
-      store8_e4m3(dst, x, kb.pages.v_scale[h]);
-      store8_e4m3(dst + 8, y, kb.pages.v_scale[h]);
-    } else {
-      store8(dst, x);
-      store8(dst + 8, y);
-    }
-    return;
-  }
-
-  const bool is_key = u >= a.units_q;
-  if (is_key) u -= a.units_q;
-  const int h = u / (DK / 16);
-  const int w = u % (DK / 16);
-  // The unit's two chunks: rotated units come first.
-  const int n_rot = rotates ? a.rot.dim >> 4 : 0;
-  const bool turn = w < n_rot;
-  int c0, c1;
   if (turn) {
-    c0 = a.rot.start + (a.rot.pairs ? 16 * w : 8 * w);
-    c1 = c0 + (a.rot.pairs ? 8 : a.rot.dim >> 1);
-  } else {
-    c0 = 16 * (w - n_rot);
-    if (rotates && c0 >= a.rot.start) c0 += a.rot.dim;
-    c1 = c0 + 8;
-  }
-  const TIn* src = is_key ? static_cast<const TIn*>(a.k.p) + row * a.k.stride + h * DK
-                          : static_cast<const TIn*>(a.q.p) + row * a.q.stride + h * DK;
-  float x[8], y[8];
-  load8(src + c0, x);
-  load8(src + c1, y);
-  if (turn) {
-    const float* cs = a.rot.cos_sin + p * a.rot.dim + 8 * w;
-    float cc[8], ss[8];
-    load8(cs, cc);
-    load8(cs + (a.rot.dim >> 1), ss);
     if (a.rot.pairs) {
       // x holds pairs 0..3 interleaved, y pairs 4..7.
 #pragma unroll
@@ -186,26 +220,31 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
       }
     }
   }
-  if (!is_key) {
+  if (!is_value && !is_key) {
     TIn* dst = static_cast<TIn*>(a.q_out) + row * a.q_out_stride + h * DK;
-    store8(dst + c0, x);
-    store8(dst + c1, y);
+    store8<NT>(dst + c0, x);
+    store8<NT>(dst + c1, y);
     return;
   }
-  TC* dst = static_cast<TC*>(kb.pages.k) + ((((int64_t)page * kb.s.Hkv + h) << kb.page_shift) + slot) * DK;
+  const int64_t place = (((int64_t)page * kb.s.Hkv + h) << kb.page_shift) + ((int)p & (kb.pages.page_size - 1));
+  TC* dst = is_value ? static_cast<TC*>(kb.pages.v) + place * DV : static_cast<TC*>(kb.pages.k) + place * DK;
   if constexpr (kE4m3) {
-    store8_e4m3(dst + c0, x, kb.pages.k_scale[h]);
-    store8_e4m3(dst + c1, y, kb.pages.k_scale[h]);
+    const float scale = (is_value ? kb.pages.v_scale : kb.pages.k_scale)[h];
+    store8_e4m3<NT>(dst + c0, x, scale);
+    store8_e4m3<NT>(dst + c1, y, scale);
   } else {
-    store8(dst + c0, x);
-    store8(dst + c1, y);
+    store8<NT>(dst + c0, x);
+    store8<NT>(dst + c1, y);
   }
 }
 
 template <int DK, int DV, typename TIn, typename TC>
 hipError_t run(const AppendArgs& a, hipStream_t st) {
-  const int64_t blocks = ((int64_t)a.kb.n_tokens * a.units + kThreads - 1) / kThreads;
-  hipLaunchKernelGGL((append_kernel<DK, DV, TIn, TC>), dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
+  const int64_t units = (int64_t)a.kb.n_tokens * a.units, blocks = (units + kThreads - 1) / kThreads;
+  if (units * 16 * (int64_t)(sizeof(TIn) + sizeof(TC)) > (int64_t)256 << 20)
+    hipLaunchKernelGGL((append_kernel<DK, DV, TIn, TC, true>), dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL((append_kernel<DK, DV, TIn, TC, false>), dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
   return hipGetLastError();
 }
 
