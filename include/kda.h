@@ -624,7 +624,7 @@ kda_status kda_attn_decode(const kda_kv_shape* shape, const kda_pages* pages, co
                            const void* q, int64_t q_stride, float scale, int32_t window, void* o, float* lse,
                            void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream);
 
-/* Bytes of kda_attn_decode's workspace; 0 for an invalid shape. */
+/* Bytes of kda_attn_decode's workspace for calls with up to shape->T new tokens; 0 for an invalid shape. */
 size_t kda_attn_workspace_bytes(const kda_kv_shape* shape, const kda_pages* pages, int32_t max_pages);
 
 /* Human-readable name of a status code (static string). */

@@ -702,7 +702,7 @@ kda_status kda_attn_decode(const kda_kv_shape* shape, const kda_pages* pages, co
   kda::KvRows qr{q, q_stride};
   if ((r = check_rows(*shape, shape->Hq, shape->dk, &qr)) != KDA_OK) return r;
   if (b.s.B == 0 || n_tokens == 0) return KDA_OK;
-  const size_t need = kda_attn_workspace_bytes(shape, pages, max_pages);
+  const size_t need = kda::attn_workspace_bytes(*shape, pages->page_size, max_pages);
   if (!q || !o || (need > 0 && !workspace)) return KDA_ERR_NULL;
   if (workspace_bytes < need) return KDA_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256)) return KDA_ERR_ALIGN;
@@ -712,7 +712,13 @@ kda_status kda_attn_decode(const kda_kv_shape* shape, const kda_pages* pages, co
 
 size_t kda_attn_workspace_bytes(const kda_kv_shape* shape, const kda_pages* pages, int32_t max_pages) {
   if (check_kv_shape(shape, pages, max_pages) != KDA_OK || !attends(*shape, pages->page_size, max_pages)) return 0;
-  return kda::attn_workspace_bytes(*shape, pages->page_size, max_pages);
+  // Calls with fewer tokens split their rows otherwise: enough for any of them.
+  size_t most = 0;
+  for (kda_kv_shape s = *shape; s.T >= 1; --s.T) {
+    const size_t n = kda::attn_workspace_bytes(s, pages->page_size, max_pages);
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 const char* kda_status_str(kda_status status) {

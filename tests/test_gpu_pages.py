@@ -497,6 +497,33 @@ def test_captured_round_replays(kda, form):
     assert b.err.item() == 0
 
 
+def test_two_graphs_that_share_a_workspace(kda):
+    """Replayed in turn, each gives what it gives alone; a workspace holds nothing between calls."""
+    a = Batch("bf16_d128", Hq=8, Hkv=2, page=64, pos=[7000, 300], counts=[2, 4], seed=34)
+    c = Batch("bf16_d128", Hq=8, Hkv=2, page=64, pos=[50, 6800], counts=[4, 1], seed=35)
+    pa, pc = a.pool(kda), c.pool(kda)
+    ws = max((kda.attn_workspace(p, x.table, Hq=8, T=4) for p, x in ((pa, a), (pc, c))), key=torch.Tensor.numel)
+    outs, graphs, plans = [], [], []
+    for b, p in ((a, pa), (c, pc)):
+        o, lse = torch.empty((b.N, 8, 128), dtype=b.dt, device="cuda"), torch.empty((b.N, 8), device="cuda")
+        plans.append(kda.AttnDecodePlan(p, b.table, b.pos, b.q, o, ws, b.err, lse=lse, tok_start=b.tok_start, T=4))
+        plans[-1]()
+        torch.cuda.synchronize()
+        outs.append((o, lse))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            plans[-1]()
+        graphs.append(g)
+    refs = [a.attend_ref(), c.attend_ref()]
+    for turn in range(3):
+        for g, (o, lse), b, ref in zip(graphs, outs, (a, c), refs):
+            o.fill_(7), lse.fill_(7)
+            g.replay()
+            torch.cuda.synchronize()
+            check_attend(o, lse, ref, b.dt, b.dk, 7004, f"turn {turn}")
+        ws.fill_(turn * 85)
+
+
 # ---------------------------------------------------------------- beside the recurrent calls
 
 def test_speculative_rounds_of_a_hybrid_stack(kda):

@@ -113,7 +113,20 @@ def test_attend_arguments(k):
     assert att(k, qst=1000) == SHAPE and att(k, qst=1028) == ALIGN
     need = k.lib().kda_attn_workspace_bytes(ctypes.byref(shp(k)), ctypes.byref(pages(k)), 4)
     assert need > 0
-    assert att(k, ws=None) == NULL and att(k, nws=need - 1) == SHAPE and att(k, ws=P(0x10080)) == ALIGN
+    assert att(k, ws=None) == NULL and att(k, nws=255) == SHAPE and att(k, ws=P(0x10080)) == ALIGN
+
+
+@pytest.mark.parametrize("kw", [dict(Hq=8, Hkv=2), dict(Hq=64, Hkv=1), dict(Hq=32, Hkv=32), dict(Hq=24, Hkv=8, dt=F32, ct=F32),
+                                dict(Hq=32, Hkv=1, dk=576, dv=512), dict(Hq=128, Hkv=1, dk=576, dv=512)])
+def test_a_workspace_serves_calls_with_fewer_tokens(k, kw):
+    sizes = [k.lib().kda_attn_workspace_bytes(ctypes.byref(shp(k, B=5, T=t, **kw)), ctypes.byref(pages(k)), 300)
+             for t in range(1, 17)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+
+
+def test_positions_are_bounded(k):
+    assert k.lib().kda_attn_workspace_bytes(ctypes.byref(shp(k, B=64)), ctypes.byref(pages(k)), 1 << 24) == 0
+    assert att(k, shp(k, B=64, T=4), N=256, cols=1 << 24) == SHAPE            # 2^36 tokens
 
 
 def test_nothing_to_do(k):
