@@ -254,6 +254,48 @@ def test_attend_latent_heads(kda, hq, T):
     run_attend(kda, b)
 
 
+@pytest.mark.parametrize("hq,T", [(64, 2), (24, 5), (16, 4), (33, 1), (32, 16)])
+@pytest.mark.parametrize("room", [1600, 6000, 40000, 1 << 18])
+def test_attend_latent_row_blocks(kda, hq, T, room):
+    """The room of the page table sets how many query rows a workgroup takes: 16 to 128."""
+    pos = [1500, 200, 31]
+    b = Batch("latent", Hq=hq, Hkv=1, page=64, pos=pos, counts=[T, 0, T], seed=31,
+              extra_cols=room // 64 - (1500 + T + 63) // 64)
+    o, lse = run_attend(kda, b)
+    o2, lse2 = b.attend(kda)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    run_attend(kda, b, "window", window=90, n_max=100)
+    ref = b.attend_ref(window=20)
+    tab = b.np_table()
+    seen = torch.zeros((b.n_pages, 64), dtype=torch.bool)
+    for s in (0, 2):
+        for p in range(pos[s] + 1 - 20, pos[s] + T):
+            seen[tab[s][p // 64], p % 64] = True
+    b.k_pages.permute(0, 2, 1, 3)[~seen.to(b.device)] = float("nan")
+    o, lse = b.attend(kda, window=20)
+    assert b.err.item() == 0
+    check_attend(o, lse, ref, b.dt, b.dk, 24 + T, "NaN around")
+    if T > 1:                                            # a NaN that only the last new token sees
+        b.k_pages[tab[2][(31 + T - 1) // 64], :, (31 + T - 1) % 64] = float("nan")
+        o, lse = b.attend(kda, window=20)
+        rows = list(range(2 * T - 1))
+        check_attend(o[rows], lse[rows], tuple(x[rows] for x in ref), b.dt, b.dk, 24 + T, "NaN in the last token")
+        assert o[-1].isnan().all()
+
+
+@pytest.mark.parametrize("room", [512, 3000, 20000, 1 << 17])
+def test_attend_latent_row_blocks_refuse_a_page(kda, room):
+    b = Batch("latent", Hq=64, Hkv=1, page=64, pos=[400, 90, 300, 7], counts=[4, 4, 4, 4], seed=32,
+              extra_cols=room // 64 - 7)
+    ref = b.attend_ref()
+    b.table[1, 1] = b.n_pages
+    o, lse = b.attend(kda)
+    assert b.err.item() == 32
+    assert (o[4:8] == 7).all() and (lse[4:8] == 7).all()
+    rows = [0, 1, 2, 3] + list(range(8, 16))
+    check_attend(o[rows], lse[rows], tuple(x[rows] for x in ref), b.dt, b.dk, 404)
+
+
 @pytest.mark.parametrize("form", ["bf16_d128", "f32_d64", "e4m3_d64", "latent"])
 @pytest.mark.parametrize("window", [1, 2, 17, 128, 1000])
 def test_attend_window(kda, form, window):
