@@ -25,11 +25,15 @@
 // and an exchange in the LDS for every tile, took 3.2 us a tile of 128 rows.
 //
 // LDS layout of a tile: 32 rows of 64 16-byte chunks (the values), then 32 rows
-// of the last 8.  Chunk c of row r lies at c ^ f(r), f(r) = r's four bits
-// rotated left by one, in the first part, and at c ^ (r / 2 % 8) in the second:
-// the key reads (16 rows, one chunk) and the transposed value reads (8 rows,
-// two neighbouring chunks) touch every bank once, and a row's first part is one
-// load of a wave, whose addresses are the row's and a constant of the lane.
+// of the last 8.  Chunk c of row r lies at c ^ f(r) in the first part, with
+// f(r) = 2 r mod 16, xor 9 from row 8 on, and at c ^ (r / 2 % 8) in the second.
+// A 16-byte read serves 16 lanes at a time, but not neighbours: lanes 0-3, 12-15
+// and 20-27, then the other 16 of the half wave (counted as conflicts: with f(r)
+// the bits of r rotated left, right for neighbours, 1024 cycles a tile).  So
+// the key reads (eight rows of one chunk, the other eight of the next) and
+// the transposed value reads (8 rows, two neighbouring chunks) touch every bank
+// once, and a row's first part is one load of a wave, whose addresses are the
+// row's and a constant of the lane.
 //
 // The outputs are scaled only when a row's maximum has grown past 2^8 times
 // the one in use: probabilities stay below 2^8 and their roundings are
@@ -54,7 +58,7 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef const __attribute__((address_space(1))) void global_void;
 
 // By row of 16.
-__device__ __forceinline__ int swizzle(int row) { return (row << 1 & 15) | (row >> 3 & 1); }
+__device__ __forceinline__ int swizzle(int row) { return (row << 1 & 14) ^ (row >> 3 & 1) * 9; }
 __device__ __forceinline__ int swizzle_tail(int row) { return row >> 1 & 7; }
 
 template <int N>
@@ -137,7 +141,7 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
             const int row = min(max(from + 4 * (wave & 3) + x, s.lo), s.end - 1) - from;
             __builtin_amdgcn_global_load_lds(
                 (global_void*)(base + row * kRowBytes +
-                               (uint32_t)((lane ^ (8 * (wave & 1) | (wave >> 1 & 1))) * 16 ^ 32 * x)),
+                               (uint32_t)((lane ^ (8 * ((wave ^ wave >> 1) & 1) | (wave >> 1 & 1))) * 16 ^ 32 * x)),
                 (lds_void*)(dst + (wave * 4 + x) * kMain), 16, 0, 0);
           }
         }
