@@ -349,9 +349,12 @@ __global__ void __launch_bounds__(DV / 4 * kJoinGroups<DV>) join_kernel(AttnArgs
 #pragma unroll
     for (int j = 0; j < FIRST; ++j) {
       const int w = w0 + share + j * split;
-      const int64_t row = row_of(min(w, w1));
-      x[j] = *reinterpret_cast<const f32x4*>(a.piece_o + row * DV + 4 * lane);
-      xm[j] = w <= w1 ? a.piece_ml[row][0] : -INFINITY;
+      const int64_t row = row_of(w);
+      x[j] = f32x4{}, xm[j] = -INFINITY;
+      if (w <= w1) {
+        x[j] = *reinterpret_cast<const f32x4*>(a.piece_o + row * DV + 4 * lane);
+        xm[j] = a.piece_ml[row][0];
+      }
     }
     const f32x2 none = {-INFINITY, 0.f};
     const f32x2 ml = w0 + same <= w1 ? a.piece_ml[row_of(w0 + same)] : none;

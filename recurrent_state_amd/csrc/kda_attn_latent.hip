@@ -122,44 +122,44 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
       auto whole = [&](int t0) { return t0 >= all_lo && t0 + kTile - 1 <= s.pos; };
       PageWalk walk(kb, s, run.b, 0);
 
-      // Tile i into buffer i % BUFS: four rows to a wave, and eight rows' last
-      // chunks to waves 0 to 3.  Rows outside the visible tokens get a copy of
-      // the nearest visible one, so that a probability of zero meets what some
-      // row sees anyway.
-      const int t16 = 16 * (wave >> 2), tail16 = 16 * (wave >> 1 & 1);
-      int32_t id = 0, tail_id = 0;  // page entries of the tile to be loaded next
-      if (n_tiles > 0) id = walk.entry(tok0 + t16), tail_id = walk.entry(tok0 + tail16);
+      // Tile i into buffer i % BUFS: four rows of a group of 16 to a wave, and
+      // eight of its rows' last chunks to two waves of each group.  Where some
+      // row is outside the visible tokens, it gets a copy of the nearest visible
+      // one, so that a probability of zero meets what some row sees anyway.
+      const int t16 = 16 * (wave >> 2);
+      const bool tails = (wave & 2) == 0;
+      int32_t id = 0;  // the page entry of the tile to be loaded next
+      if (n_tiles > 0) id = walk.entry(tok0 + t16);
       auto load = [&](int i) {
-        const int tok = tok0 + i * kTile, lane = here((int)threadIdx.x & 63);
+        const int tok = tok0 + i * kTile + t16, lane = here((int)threadIdx.x & 63);
         unsigned char* dst = lds + i % BUFS * kBufBytes;
-        const unsigned char* pages = static_cast<const unsigned char*>(kb.pages.k);
-        {
-          const unsigned char* base = pages + walk.row(tok + t16, id) * kRowBytes;
-          const int from = min(max(tok + t16, walk.lo), walk.hi);  // the token of the base row
+        const unsigned char* base = static_cast<const unsigned char*>(kb.pages.k) + walk.row(tok, id) * kRowBytes;
+        const uint32_t at = (lane ^ (8 * ((wave ^ wave >> 1) & 1) | (wave >> 1 & 1))) * 16;
+        const int r = 8 * (wave & 1) + (lane >> 3);  // of the tails
+        const uint32_t tail_at = kMain + ((lane & 7) ^ swizzle_tail(r)) * 16;
+        auto get = [&](uint32_t offset, unsigned char* to) {
+          __builtin_amdgcn_global_load_lds((global_void*)(base + offset), (lds_void*)to, 16, 0, 0);
+        };
+        unsigned char* rows = dst + wave * 4 * kMain;
+        unsigned char* tail = dst + kTailAt + (2 * (wave >> 2) + (wave & 1)) * 8 * kTail;
+        if (tok >= s.lo && tok + 16 <= s.end) {
+          const uint32_t row = 4 * (wave & 3) * kRowBytes;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int row = min(max(from + 4 * (wave & 3) + x, s.lo), s.end - 1) - from;
-            __builtin_amdgcn_global_load_lds(
-                (global_void*)(base + row * kRowBytes +
-                               (uint32_t)((lane ^ (8 * ((wave ^ wave >> 1) & 1) | (wave >> 1 & 1))) * 16 ^ 32 * x)),
-                (lds_void*)(dst + (wave * 4 + x) * kMain), 16, 0, 0);
-          }
+          for (int x = 0; x < 4; ++x) get((at ^ 32 * x) + (row + x * kRowBytes), rows + x * kMain);
+          if (tails) get(r * kRowBytes + tail_at, tail);
+        } else {
+          const int from = min(max(tok, walk.lo), walk.hi);  // the token of the base row
+          auto near = [&](int row) { return (uint32_t)(min(max(from + row, s.lo), s.end - 1) - from); };  // 0 to 15
+#pragma unroll
+          for (int x = 0; x < 4; ++x) get((at ^ 32 * x) + near(4 * (wave & 3) + x) * kRowBytes, rows + x * kMain);
+          if (tails) get(near(r) * kRowBytes + tail_at, tail);
         }
-        if (wave < 4) {
-          const unsigned char* base = pages + walk.row(tok + tail16, tail_id) * kRowBytes + kMain;
-          const int from = min(max(tok + tail16, walk.lo), walk.hi);
-          const int r = 8 * (wave & 1) + (lane >> 3), row = min(max(from + r, s.lo), s.end - 1) - from;
-          __builtin_amdgcn_global_load_lds(
-              (global_void*)(base + (uint32_t)(row * kRowBytes + ((lane & 7) ^ swizzle_tail(r)) * 16)),
-              (lds_void*)(dst + kTailAt + wave * 8 * kTail), 16, 0, 0);
-        }
-        id = walk.entry(tok + kTile + t16);
-        tail_id = walk.entry(tok + kTile + tail16);
+        id = walk.entry(tok + kTile);
       };
       // Waits until tile i has landed; tiles up to `issued` are on their way.
       auto landed = [&](int i, int issued) {
         const int behind = issued - i;
-        if (wave < 4) {
+        if (tails) {
           if (BUFS == 4 && behind >= 2)
             wait_loads<10>();
           else if (behind >= 1)
