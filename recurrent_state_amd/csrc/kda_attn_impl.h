@@ -317,7 +317,7 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
 // rows of a (sequence, kv head).  Every wave finds m and the sum by itself, a
 // piece to a lane.
 template <int DV>
-constexpr int kJoinFirst = DV == 512 ? 8 : 4;  // pieces of a row that a group asks for at once
+constexpr int kJoinFirst = DV == 512 ? 6 : 4;  // pieces of a row that a group asks for at once
 template <int DV>
 constexpr int kJoinGroups = DV == 512 ? 8 : 16;  // of a workgroup, at most
 
@@ -337,57 +337,64 @@ __global__ void __launch_bounds__(DV / 4 * kJoinGroups<DV>) join_kernel(AttnArgs
   const int r0 = blockIdx.z * rows_each, r1 = min(r0 + rows_each, sr.n * G);
   if (r0 >= r1) return;
   const float vs = kb.pages.v_scale ? kb.pages.v_scale[hk] : 1.f;
+  // Piece d of the sequence is worker w0 + d's: rows from the first worker's
+  // first slot on (a workspace is far below 2^32 bytes).
+  const int pieces = w1 - w0 + 1;
+  const uint32_t slot = (uint32_t)kb.s.Hkv * a.row_blocks * a.rows;
+  const char* outs = reinterpret_cast<const char*>(a.piece_o + (int64_t)w0 * 2 * slot * DV);
+  const char* stats = reinterpret_cast<const char*>(a.piece_ml + (int64_t)w0 * 2 * slot);
   for (int rr = r0; rr < r1; rr += rows_at_once) {
     const bool live = rr + group / split < r1;
     const int r = live ? rr + group / split : r0;
-    const int rb = r / a.rows, in = r % a.rows;
-    const auto row_of = [&](int w) { return piece_index(a, w, w == w0 ? 1 : 0, hk, rb) * a.rows + in; };
+    const uint32_t at = ((uint32_t)hk * a.row_blocks + r / a.rows) * a.rows + r % a.rows;
+    const auto row_of = [&](int d) { return (d == 0 ? slot : 2u * d * slot) + at; };
+    const auto out = [&](int d) {
+      return *reinterpret_cast<const f32x4*>(outs + (row_of(d) * (uint32_t)(DV * 4) + 16u * lane));
+    };
+    const auto stat = [&](int d) { return *reinterpret_cast<const f32x2*>(stats + row_of(d) * 8u); };
     // The first pieces' outputs are asked for before their weights are known.
     constexpr int FIRST = kJoinFirst<DV>;
     f32x4 x[FIRST];
     float xm[FIRST];
 #pragma unroll
     for (int j = 0; j < FIRST; ++j) {
-      const int w = w0 + share + j * split;
-      const int64_t row = row_of(w);
+      const int d = share + j * split;
       x[j] = f32x4{}, xm[j] = -INFINITY;
-      if (w <= w1) {
-        x[j] = *reinterpret_cast<const f32x4*>(a.piece_o + row * DV + 4 * lane);
-        xm[j] = a.piece_ml[row][0];
-      }
+      if (d < pieces) x[j] = out(d), xm[j] = stat(d)[0];
     }
     const f32x2 none = {-INFINITY, 0.f};
-    const f32x2 ml = w0 + same <= w1 ? a.piece_ml[row_of(w0 + same)] : none;
+    const f32x2 ml = same < pieces ? stat(same) : none;
     float m = ml[0];
     int refused = ml[1] < 0.f;
-    for (int w = w0 + same + SAME; w <= w1; w += SAME) {
-      const f32x2 y = a.piece_ml[row_of(w)];
+    for (int d = same + SAME; d < pieces; d += SAME) {
+      const f32x2 y = stat(d);
       m = fmaxf(m, y[0]);
       refused |= y[1] < 0.f;
     }
     // Every row of the sequence comes out the same, so the workgroup agrees.
     if (__ballot(refused) != 0) return;
 #pragma unroll
-    for (int d = 1; d < SAME; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
+    for (int i = 1; i < SAME; i *= 2) m = fmaxf(m, __shfl_xor(m, i));
     // A piece in which the row sees no token has m = -inf and zeros.
     const float top = m == -INFINITY ? 0.f : m;
     float l = ml[1] * exp2_(ml[0] - top);
-    for (int w = w0 + same + SAME; w <= w1; w += SAME) {
-      const f32x2 y = a.piece_ml[row_of(w)];
+    for (int d = same + SAME; d < pieces; d += SAME) {
+      const f32x2 y = stat(d);
       l += y[1] * exp2_(y[0] - top);
     }
 #pragma unroll
-    for (int d = 1; d < SAME; d *= 2) l += __shfl_xor(l, d);
+    for (int i = 1; i < SAME; i *= 2) l += __shfl_xor(l, i);
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < FIRST; ++j)
+    for (int j = 0; j < FIRST; ++j) {
+      const float f = exp2_(xm[j] - top);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] += w0 + share + j * split <= w1 ? x[j][i] * exp2_(xm[j] - top) : 0.f;
+      for (int i = 0; i < 4; ++i) o[i] += x[j][i] * f;
+    }
 #pragma unroll 4
-    for (int w = w0 + share + FIRST * split; w <= w1; w += split) {
-      const int64_t row = row_of(w);
-      const float f = exp2_(a.piece_ml[row][0] - top);
-      const f32x4 y = *reinterpret_cast<const f32x4*>(a.piece_o + row * DV + 4 * lane);
+    for (int d = share + FIRST * split; d < pieces; d += split) {
+      const float f = exp2_(stat(d)[0] - top);
+      const f32x4 y = out(d);
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] += y[i] * f;
     }
