@@ -24,6 +24,10 @@
 // over pairs of waves, which halves the key reads but needs a second barrier
 // and an exchange in the LDS for every tile, took 3.2 us a tile of 128 rows.
 //
+// Measured: a tile of 128 rows takes 2.7 us on every CU (840 TFLOP/s; the MFMAs
+// are busy for a third of it, and neither deeper LDS read-ahead nor loads
+// spread over the products shortened it), and up to 32 rows read at 5.1 TB/s.
+//
 // LDS layout of a tile: 32 rows of 64 16-byte chunks (the values), then 32 rows
 // of the last 8.  Chunk c of row r lies at c ^ f(r) in the first part, with
 // f(r) = 2 r mod 16, xor 9 from row 8 on, and at c ^ (r / 2 % 8) in the second.

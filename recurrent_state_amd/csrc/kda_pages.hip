@@ -11,7 +11,9 @@
 //
 // Bound by memory for prompts, and by the chain of dependent loads (token range,
 // position, page) for a few tokens: the unit's values depend on none of these
-// and are asked for first.
+// and are asked for first.  Measured, 32 query and 8 kv heads of 128 in bf16:
+// eight prompts of 8192 tokens 290 us (1.64 GB, 5.7 TB/s), one token 2.6 us;
+// 256 tokens of a latent cache 6.5 us.
 
 #include "kda_pages.h"
 
@@ -238,6 +240,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
   }
 }
 
+// Calls that touch more than the 256 MB Infinity Cache go past it: 65536 tokens
+// of 32 + 8 heads of 128 in 319 -> 290 us.  What smaller calls write stays there
+// for the attention that reads it next.
 template <int DK, int DV, typename TIn, typename TC>
 hipError_t run(const AppendArgs& a, hipStream_t st) {
   const int64_t units = (int64_t)a.kb.n_tokens * a.units, blocks = (units + kThreads - 1) / kThreads;
