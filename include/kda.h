@@ -591,7 +591,9 @@ typedef struct kda_rotation {
  * table (KDA_DEV_ERR_POS), or past the page table or on a page outside
  * [0, n_pages) (KDA_DEV_ERR_PAGE), is skipped, its q_out row included.  Two
  * tokens of one call must not share a place (sequences may share pages of a
- * common prefix, which no call writes).  dev_err must not be NULL.
+ * common prefix, which no call writes).  n_tokens times the 16-value units of a
+ * token's rows, (Hq dk + Hkv (dk + dv)) / 16, is below 2^32 - 256.  dev_err must
+ * not be NULL.
  */
 kda_status kda_kv_append(const kda_kv_shape* shape, const kda_pages* pages, const int32_t* table, int32_t max_pages,
                          const int32_t* tok_start, int32_t n_tokens, const int64_t* pos, const void* k,
@@ -608,14 +610,17 @@ kda_status kda_kv_append(const kda_kv_shape* shape, const kda_pages* pages, cons
  * the cache, so they are appended first.  A row that sees no token (p < 0)
  * gets o = 0 and lse = -inf.  Tokens that a row does not see do not reach it,
  * whatever they hold.  1 <= T <= 16 (a decode token, or the drafts of a
- * speculative round), B * max_pages * page_size at most about 2^35 tokens.  scale normally 1/sqrt of the width the model trained
- * with; it must be finite.
+ * speculative round), B <= 2^20, B * max_pages * page_size at most about
+ * 2^35 tokens.  scale normally 1/sqrt of the width the model trained with; it
+ * must be finite.
  * A sequence whose visible tokens run past the page table or lie on a page
  * outside [0, n_pages) sets KDA_DEV_ERR_PAGE and is skipped.
  * workspace: kda_attn_workspace_bytes(shape, pages, max_pages) bytes of
  * device memory, 256-byte aligned, holding nothing between calls; calls that
  * may run at the same time need one each.  The cache's split over the chip
- * depends on the positions only, so equal calls give equal bits.
+ * depends on the shape, max_pages and the positions only, so equal calls give
+ * equal bits.  A latent cache is split more finely where max_pages leaves room
+ * for little: a table no wider than its sequences need is faster.
  * (vLLM blog, Part 1, section 2: decode attention whose cache is split, and
  * whose partial results one kernel combines.)
  */

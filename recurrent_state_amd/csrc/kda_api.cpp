@@ -141,9 +141,10 @@ kda_status check_kv_shape(const kda_kv_shape* s, const kda_pages* pages, int32_t
   return KDA_OK;
 }
 
-// kda_attn_decode counts the tiles (32 tokens or more) of all sequences in 32 bits.
+// kda_attn_decode counts the tiles (32 tokens or more) of all sequences in 32
+// bits, and its join has a block of up to 1024 threads to each sequence.
 bool attends(const kda_kv_shape& s, int32_t page_size, int32_t max_pages) {
-  return s.T <= kMaxT && (int64_t)s.B * ((int64_t)max_pages * page_size / 32 + 2) <= (int64_t)1 << 30;
+  return s.T <= kMaxT && s.B <= 1 << 20 && (int64_t)s.B * ((int64_t)max_pages * page_size / 32 + 2) <= (int64_t)1 << 30;
 }
 
 // Everything the two calls share; fills in `b` on success.
@@ -154,9 +155,9 @@ kda_status check_kv(const kda_kv_shape* s, const kda_pages* pages, const int32_t
   if (r != KDA_OK) return r;
   if (n_tokens < 0 || n_tokens > 1 << 30) return KDA_ERR_SHAPE;
   if (!tok_start && (int64_t)n_tokens != (int64_t)s->B * s->T) return KDA_ERR_SHAPE;
-  // A grid of one 256-thread block per 256 units of 16 values must fit.
+  // A thread to each unit of 16 values, and a launch has below 2^32 of them.
   const int64_t units = ((int64_t)s->Hq * s->dk + (int64_t)s->Hkv * (s->dk + s->dv)) / 16;
-  if ((int64_t)n_tokens * units > (int64_t)1 << 38) return KDA_ERR_SHAPE;
+  if ((int64_t)n_tokens * units > ((int64_t)1 << 32) - 256) return KDA_ERR_SHAPE;
   if (s->B > 0 && n_tokens > 0) {
     const bool latent = is_latent(*s);
     if (pages->n_pages < 1) return KDA_ERR_SHAPE;

@@ -129,22 +129,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
 
   // Row and unit of this thread; the threads past the last unit take part in
   // seq_of_row with that one's row.
-  const int64_t total = (int64_t)kb.n_tokens * a.units;
-  int row, u;
-  bool live = true;
-  if (total <= (int64_t)1 << 31) {
-    const uint32_t e = blockIdx.x * kThreads + threadIdx.x;
-    live = e < (uint32_t)total;
-    const uint32_t at = live ? e : (uint32_t)total - 1;
-    row = (int)(at / (uint32_t)a.units);
-    u = (int)(at - (uint32_t)row * (uint32_t)a.units);
-  } else {
-    const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    live = e < total;
-    const int64_t at = live ? e : total - 1;
-    row = (int)(at / a.units);
-    u = (int)(at - (int64_t)row * a.units);
-  }
+  const uint32_t total = (uint32_t)kb.n_tokens * (uint32_t)a.units;  // fits: checked on the host
+  const uint32_t e = blockIdx.x * kThreads + threadIdx.x;
+  const bool live = e < total;
+  const uint32_t unit = live ? e : total - 1;
+  const int row = (int)(unit / (uint32_t)a.units), u = (int)(unit - (uint32_t)row * (uint32_t)a.units);
 
   // What the unit is, and its two chunks: rotated units of a head come first.
   const bool is_value = u >= a.units_k, is_key = !is_value && u >= a.units_q;

@@ -89,6 +89,18 @@ def test_tables_and_tokens(k):
                                  None) == NULL
 
 
+def test_launches_fit_the_grid(k):
+    s = shp(k, B=1, T=1 << 26)                            # 96 units of 16 values to a token
+    most = ((1 << 32) - 256) // 96
+    for N in (most + 1, 1 << 26):
+        assert app(k, s, ts=GOOD, N=N) == SHAPE
+    assert app(k, s, ts=GOOD, N=most, kr=None) == NULL    # passes that check, and is stopped at the next one
+    many = shp(k, B=(1 << 20) + 1, T=1)
+    assert att(k, many, ts=GOOD, N=8, cols=1) == SHAPE
+    assert k.lib().kda_attn_workspace_bytes(ctypes.byref(many), ctypes.byref(pages(k)), 1) == 0
+    assert att(k, shp(k, B=1 << 20, T=1), ts=GOOD, N=8, cols=1, q=None) == NULL
+
+
 def test_append_arguments(k):
     rot = lambda cs=0x10000, mp=64, start=0, dim=128, pairs=0: k._lib._Rotation(cs, mp, start, dim, pairs)  # noqa: E731
     assert app(k, kr=None) == NULL and app(k, v=None) == NULL
