@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
               store8(a.piece_o + row * D + c0, o);
               if (c0 == 0) a.piece_ml[row] = (f32x2){M, bad ? -1.f : L};
             } else if (!bad) {
-              const float inv = L == 0.f ? 0.f : v_scale / L;
+              const float inv = s.pos + r / G < 0 ? 0.f : v_scale / L;  // 0 / 0 where every score is -inf
 #pragma unroll
               for (int i = 0; i < 8; ++i) o[i] *= inv;
               const int64_t row = (int64_t)(s.row0 + r / G) * kb.s.Hq + hk * G + r % G;

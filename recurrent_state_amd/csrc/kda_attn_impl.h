@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(DV / 4 * kJoinGroups<DV>) join_kernel(AttnArgs
   const int w0 = a.span[b].x, w1 = a.span[b].y;
   if (w0 == w1) return;
   const int G = kb.s.Hq / kb.s.Hkv;
+  const int64_t pos = kb.pos[b];
   const SeqRows sr = seq_rows(kb, b);
   constexpr int SAME = LANES < kWave ? LANES : kWave;  // lanes of a wave that hold one row
   const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES, same = threadIdx.x % SAME;
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(DV / 4 * kJoinGroups<DV>) join_kernel(AttnArgs
       __syncthreads();
     }
     if (live && share == 0) {
-      const float inv = l == 0.f ? 0.f : vs / l;
+      const float inv = pos + r / G < 0 ? 0.f : vs / l;  // 0 / 0 where every score is -inf
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] *= inv;
       const int64_t row = (int64_t)(sr.row0 + r / G) * kb.s.Hq + hk * G + r % G;

@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
           for (int c = 0; c < kCols; ++c) store4(a.piece_o + row * kDv + c0 + 16 * c, held[n * kCols + c]);
           if (c0 == 0) a.piece_ml[row] = (f32x2){ml[0], bad ? -1.f : ml[1]};
         } else if (!bad) {
-          const float inv = ml[1] == 0.f ? 0.f : 1.f / ml[1];
+          const float inv = s.pos + r / Hq < 0 ? 0.f : 1.f / ml[1];  // 0 / 0 where every score is -inf
           const int64_t row = (int64_t)(s.row0 + r / Hq) * Hq + r % Hq;
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {

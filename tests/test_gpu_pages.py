@@ -364,6 +364,27 @@ def test_hidden_tokens_do_not_reach_a_row(kda, form, junk):
 
 
 @pytest.mark.parametrize("form", ["bf16_d128", "f32_d64", "latent"])
+def test_scores_of_minus_infinity(kda, form):
+    """Keys of -inf weigh nothing beside others, and make 0 / 0 where a row sees nothing else, as in the formula."""
+    b = Batch(form, **heads(form, 4, 2), page=64, pos=[40, 9000, -1], counts=[2, 1, 1], seed=33)
+    col, tab = 570 if b.latent else 5, b.np_table()
+    b.q[..., col] = 1.0
+    one = [(tab[0][0], 7), (tab[1][0], 7)]               # token 7 of both
+    keys = [b.k_pages[pg, :, at].clone() for pg, at in one]
+    b.k_pages[..., col] = -float("inf")
+    o, lse = b.attend(kda)
+    assert o[:3].isnan().all() and (o[3] == 0).all() and lse.isneginf().all()
+    for (pg, at), key in zip(one, keys):
+        b.k_pages[pg, :, at] = key
+    o, lse = b.attend(kda)
+    assert b.err.item() == 0
+    for row, (pg, at) in zip((0, 1, 2), (one[0], one[0], one[1])):
+        v = b.k_pages[pg, :, at, :512] if b.latent else b.v_pages[pg, :, at]
+        assert torch.equal(o[row], v.repeat_interleave(b.Hq // b.Hkv, 0))
+    assert lse[:3].isfinite().all() and (o[3] == 0).all()
+
+
+@pytest.mark.parametrize("form", ["bf16_d128", "f32_d64", "latent"])
 def test_nan_in_a_seen_value_reaches_its_column_only(kda, form):
     b = Batch(form, **heads(form), page=16, pos=[300], counts=[2], seed=22)
     tab = b.np_table()
