@@ -9,11 +9,14 @@
 //                   equal run: a batch of long and short sequences keeps every
 //                   CU busy to the end.  A run may hold whole sequences, whose
 //                   outputs its worker writes itself, and at most two pieces
-//                   of others.
-//   few (two workers or more to each of up to 64)  Every worker takes a piece
-//                   of one sequence, of the shortest length with which the
-//                   workers suffice: somewhat less even, but a worker loads
-//                   queries and writes results once.
+//                   of others.  Where one more sequence in a run costs its
+//                   worker much (queries to load, a piece to write), each
+//                   sequence begins with some places of the list that stand
+//                   for this and hold no tile.
+//   few (up to 64, with `few` workers or more to each)  Every worker takes a
+//                   piece of one sequence, of the shortest length with which
+//                   the workers suffice: somewhat less even, but a worker
+//                   loads queries and writes results once.
 // Pieces go to the workspace (slot 0: a sequence that an earlier worker began,
 // slot 1: the others) and are joined, in the workers' order, by a second kernel.
 #pragma once
@@ -40,6 +43,8 @@ struct AttnArgs {
   float* lse;
   int32_t workers;     // runs of the tile list at most
   int32_t run_tiles;   // tiles of a run at least, while there are enough
+  int32_t start_tiles; // what a sequence's beginning costs a worker, in tiles
+  int32_t few;         // workers to a sequence, from which on each takes one piece
   int32_t row_blocks;  // blocks of query rows of a (sequence, kv head)
   int32_t rows;        // query rows of a block
   // Workspace: each sequence's first and last worker [B], then for every piece
@@ -135,7 +140,7 @@ __device__ __forceinline__ int32_t wave_scan(int32_t x) {
   return x;
 }
 
-// How `total` tiles fall to the workers: `count` of them have a run (none is
+// How `total` places of the list fall to the workers: `count` of them have a run (none is
 // empty), the first `more` of one tile more than the others' `each`.
 struct Shares {
   uint32_t count, each, more;
@@ -152,8 +157,8 @@ struct Shares {
   }
 };
 
-// A worker's run [tile, end) of the tile list, and the sequence that it is at:
-// number b, whose own tiles begin at `first`.
+// A worker's run [tile, end) of the list, and the sequence that it is at: number
+// b, whose own tiles begin at `first`.
 template <int TILE>
 struct Run {
   const AttnArgs& a;
@@ -170,11 +175,11 @@ struct Run {
     int32_t total = 0, upto = 0;
     for (int c = 0; c < B; c += kWave) {
       lanes = c + lane < B ? seq_of<TILE>(a, c + lane) : Seq{};
-      upto = wave_scan(lanes.tiles);
+      upto = wave_scan(places(lanes));
       if (record && lanes.err) set_err(a.kb.dev_err, lanes.err);
       total += __builtin_amdgcn_readlane(upto, kWave - 1);
     }
-    if (B <= kWave && 2 * B <= a.workers) {
+    if (B <= kWave && a.few * B <= a.workers) {
       one_piece(worker, record, lanes, total);
       return;
     }
@@ -188,7 +193,7 @@ struct Run {
     if (B > kWave) {
       for (; b < B; b += kWave) {
         lanes = b + lane < B ? seq_of<TILE>(a, b + lane) : Seq{};
-        upto = wave_scan(lanes.tiles);
+        upto = wave_scan(places(lanes));
         const int32_t sum = __builtin_amdgcn_readlane(upto, kWave - 1);
         if (record) write_span(shares, b + lane, before + upto, lanes.tiles);
         // The recording wave goes through all of them; its worker is the first.
@@ -200,7 +205,7 @@ struct Run {
         if (tile < end) {  // back to the first sequence with tiles
           for (; b < B; b += kWave) {
             lanes = b + lane < B ? seq_of<TILE>(a, b + lane) : Seq{};
-            upto = wave_scan(lanes.tiles);
+            upto = wave_scan(places(lanes));
             if (__builtin_amdgcn_readlane(upto, kWave - 1) > 0) break;
           }
         }
@@ -213,6 +218,7 @@ struct Run {
     const int at = uniform(__ffsll((unsigned long long)__ballot(before + upto > tile)) - 1);
     b += at;
     first = before + __builtin_amdgcn_readlane(upto - lanes.tiles, at);
+    tile = max(tile, first);
     s = seq_of_lane(lanes, at);
   }
 
@@ -220,6 +226,7 @@ struct Run {
   __device__ __forceinline__ void one_piece(int worker, bool record, const Seq& lanes, int32_t total) {
     const int lane = threadIdx.x & 63;
     const int busy = __popcll(__ballot(lanes.tiles > 0));
+    total -= busy * a.start_tiles;
     // Of n pieces of a sequence the last is half empty on average.
     int32_t each = max(a.run_tiles, (int)((uint32_t)total / (uint32_t)(a.workers - busy / 2)));
     int32_t count, upto;
@@ -239,7 +246,10 @@ struct Run {
     end = shares.begin(piece + 1);
   }
 
-  // Sequence `seq`, whose tiles end before tile `upto`.
+  // A sequence's places in the list: its tiles come last.
+  __device__ __forceinline__ int32_t places(const Seq& x) const { return x.tiles > 0 ? x.tiles + a.start_tiles : 0; }
+
+  // Sequence `seq`, whose tiles end before place `upto`.
   __device__ __forceinline__ void write_span(const Shares& shares, int seq, int32_t upto, int32_t tiles) const {
     if (seq < a.kb.s.B)
       a.span[seq] = tiles > 0 ? make_int2(shares.of(upto - tiles), shares.of(upto - 1)) : make_int2(0, 0);
@@ -257,6 +267,8 @@ struct Run {
       }
       s = seq_of_lane(seq_of<TILE>(a, b), 0);
     } while (s.tiles == 0);
+    first += a.start_tiles;
+    tile = first;
   }
 };
 
@@ -431,7 +443,7 @@ inline bool outgrows_cache(const KvBatch& kb) {
 
 // How a call is split: see split_of() of each kernel.
 struct Split {
-  int tile, rows, row_blocks, workers, run_tiles;
+  int tile, rows, row_blocks, workers, run_tiles, start_tiles, few;
 };
 
 // Workers for `wgs` workgroups on the chip at once: at most one to a shortest
@@ -463,7 +475,7 @@ inline AttnArgs make_args(const KvBatch& b, KvRows q, float scale, int32_t windo
   return AttnArgs{b,         q,
                   scale,     window,
                   o,         lse,
-                  d.workers, d.run_tiles, d.row_blocks,
+                  d.workers, d.run_tiles, d.start_tiles, d.few, d.row_blocks,
                   d.rows,    reinterpret_cast<int2*>(ws),
                   reinterpret_cast<f32x2*>(ws + L.ml), reinterpret_cast<float*>(ws + L.o)};
 }

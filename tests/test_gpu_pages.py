@@ -319,6 +319,17 @@ def test_attend_many_sequences(kda):
         run_attend(kda, b, form)
 
 
+@pytest.mark.parametrize("B,hq,T", [(60, 32, 4), (150, 16, 2), (66, 64, 3), (200, 1, 1)])
+def test_attend_latent_batches_of_uneven_sequences(kda, B, hq, T):
+    """Runs of the list of tiles that begin, end and pass over sequences of one tile and of many, idle ones between."""
+    rng = np.random.default_rng(B)
+    pos = rng.choice([-1, 0, 31, 40, 300, 1300], B, p=[0.05, 0.2, 0.2, 0.3, 0.15, 0.1])
+    counts = rng.integers(0, T + 1, B)
+    b = Batch("latent", Hq=hq, Hkv=1, page=32, pos=pos, counts=counts, seed=34)
+    run_attend(kda, b)
+    run_attend(kda, b, "window", window=33, n_max=64)
+
+
 @pytest.mark.parametrize("form", ["bf16_d128", "f32_d64", "latent"])
 def test_attend_scales(kda, form):
     b = Batch(form, **heads(form), page=16, pos=[100, 257], counts=[1, 2], seed=20)
