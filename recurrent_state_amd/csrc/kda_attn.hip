@@ -29,8 +29,8 @@
 //
 // Measured with the join, 32 heads over 8 of 128, one new token each: one
 // sequence of 131071 tokens 92 us (537 MB, 5.8 TB/s), 64 of 60 to 8191 tokens
-// 84 us (446 MB, 5.3 TB/s), 32 of 4000 to 16001 tokens in e4m3 103 us (569 MB,
-// 5.5 TB/s): at the rate of memory.  One sequence of 1021 tokens takes 10.5 us,
+// 80 us (446 MB, 5.6 TB/s), 32 of 4000 to 16001 tokens in e4m3 97 us (571 MB,
+// 5.9 TB/s): at the rate of memory.  One sequence of 1021 tokens takes 10.3 us,
 // which is two launches and the chain positions, page, keys, values.
 //
 // Rounding: scores, maxima, sums and outputs are fp32; for bf16 queries the
