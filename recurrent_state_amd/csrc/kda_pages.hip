@@ -99,9 +99,10 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&x)[8], flo
   put<NT>(reinterpret_cast<u32x2*>(p), (u32x2){(uint32_t)w[0], (uint32_t)w[1]});
 }
 
-// The sequence of packed row `row`: the last one that starts at or before it.
-// The wave finds its first row's sequence by counting starts, 64 at a time;
-// the lanes go on from there (a wave spans few rows).
+// The sequence of packed row `row`: the last one that starts at or before it,
+// or -1 for a row before the first one's.  The wave finds its first row's
+// sequence (-1 too) by counting starts, 64 at a time; the lanes go on from
+// there (a wave spans few rows).
 __device__ __forceinline__ int seq_of_row(const KvBatch& kb, int row) {
   const int lane = threadIdx.x & 63;
   const int first = __builtin_amdgcn_readfirstlane(row);
@@ -112,7 +113,6 @@ __device__ __forceinline__ int seq_of_row(const KvBatch& kb, int row) {
     b += n;
     if (n < kWave) break;
   }
-  if (b < 0) return -1;
   while (b + 1 < kb.s.B && kb.tok_start[b + 1] <= row) ++b;
   return b;
 }
