@@ -17,10 +17,14 @@ struct SeqRows {
   int32_t row0, n;
   bool bad;
 };
+// Whether rows r0 .. r1 - 1 can be a sequence's.
+__device__ __forceinline__ bool fits(const KvBatch& kb, int64_t r0, int64_t r1) {
+  return r0 >= 0 && r1 >= r0 && r1 <= kb.n_tokens && r1 - r0 <= kb.s.T;
+}
 __device__ __forceinline__ SeqRows seq_rows(const KvBatch& kb, int b) {
   if (!kb.tok_start) return SeqRows{b * kb.s.T, kb.s.T, false};
   const int64_t r0 = kb.tok_start[b], r1 = kb.tok_start[b + 1];
-  if (r0 < 0 || r1 < r0 || r1 > kb.n_tokens || r1 - r0 > kb.s.T) return SeqRows{0, 0, true};
+  if (!fits(kb, r0, r1)) return SeqRows{0, 0, true};
   return SeqRows{(int32_t)r0, (int32_t)(r1 - r0), false};
 }
 

@@ -99,22 +99,44 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&x)[8], flo
   put<NT>(reinterpret_cast<u32x2*>(p), (u32x2){(uint32_t)w[0], (uint32_t)w[1]});
 }
 
-// The sequence of packed row `row`: the last one that starts at or before it,
-// or -1 for a row before the first one's.  The wave finds its first row's
-// sequence (-1 too) by counting starts, 64 at a time; the lanes go on from
-// there (a wave spans few rows).
-__device__ __forceinline__ int seq_of_row(const KvBatch& kb, int row) {
-  const int lane = threadIdx.x & 63;
-  const int first = __builtin_amdgcn_readfirstlane(row);
-  int b = -1;
-  for (int c = 0; c < kb.s.B; c += kWave) {
-    const bool before = c + lane < kb.s.B && kb.tok_start[c + lane] <= first;
-    const int n = __popcll(__ballot(before));
-    b += n;
-    if (n < kWave) break;
+// A sequence with packed row `row` in its range, and which of its tokens that
+// row is; b = -1 for a row of no sequence.
+struct Owner {
+  int b, token;
+  bool more;  // a later sequence's range holds the row too
+};
+// The first such sequence from `from` on.  Every range counts by itself, so that
+// one that does not fit the launch takes nothing from the others, wherever its
+// ends point.  All of them are looked at, a lane taking four of 256 neighbours
+// (the rest 64 at a time), and the few that meet the wave's rows, which ascend
+// with the lanes, are held against each lane's.
+__device__ __forceinline__ Owner owner_of(const KvBatch& kb, int row, int from) {
+  const int lane = threadIdx.x & 63, B = kb.s.B;
+  const int first = __builtin_amdgcn_readfirstlane(row), last = __builtin_amdgcn_readlane(row, kWave - 1);
+  Owner o{-1, 0, false};
+  auto meet = [&](int c, int step, int32_t start, int32_t end) {  // of sequence c + step * lane
+    for (uint64_t near = __ballot(start <= last && end > first); near != 0; near &= near - 1) {
+      const int at = __ffsll((unsigned long long)near) - 1, b = c + step * at;
+      const int r0 = __builtin_amdgcn_readlane(start, at), r1 = __builtin_amdgcn_readlane(end, at);
+      if (!fits(kb, r0, r1) || row < r0 || row >= r1 || b < from) continue;
+      o.more |= o.b >= 0;
+      if (o.b < 0 || b < o.b) o.b = b, o.token = row - r0;
+    }
+  };
+  int c = 0;
+  for (; c + 4 * kWave <= B; c += 4 * kWave) {
+    const int32_t* p = kb.tok_start + c + 4 * lane;
+    int32_t at[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) at[j] = p[j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) meet(c + j, 4, at[j], at[j + 1]);
   }
-  while (b + 1 < kb.s.B && kb.tok_start[b + 1] <= row) ++b;
-  return b;
+  for (; c < B; c += kWave) {
+    const int b = min(c + lane, B - 1);
+    meet(c, 1, kb.tok_start[b], c + lane < B ? kb.tok_start[b + 1] : INT32_MIN);
+  }
+  return o;
 }
 
 template <int DK, int DV, typename TIn, typename TC, bool NT>
@@ -128,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
       if (seq_rows(kb, b).bad) set_err(kb.dev_err, KDA_DEV_ERR_TOKENS);
 
   // Row and unit of this thread; the threads past the last unit take part in
-  // seq_of_row with that one's row.
+  // owner_of with that one's row.
   const uint32_t total = (uint32_t)kb.n_tokens * (uint32_t)a.units;  // fits: checked on the host
   const uint32_t e = blockIdx.x * kThreads + threadIdx.x;
   const bool live = e < total;
@@ -163,69 +185,79 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
                  : static_cast<const TIn*>(a.q.p) + row * a.q.stride + h * DK;
   }
   float x[8], y[8];
-  load8<NT>(src + c0, x);
-  load8<NT>(src + c1, y);
 
-  const int b = kb.tok_start ? seq_of_row(kb, row) : row / kb.s.T;
-  if (!live || b < 0) return;
-  const int64_t pos = kb.pos[b];
-  const SeqRows sr = seq_rows(kb, b);
-  const int i = row - sr.row0;
-  if (sr.bad || i < 0 || i >= sr.n) return;
-  const int64_t p = pos + i;
-  if (p < 0 || (rotates && p >= a.rot.max_pos)) {
-    if (u == 0) set_err(kb.dev_err, KDA_DEV_ERR_POS);
-    return;
-  }
-  const int64_t at = p >> kb.page_shift;
-  const int32_t page = at < kb.max_pages ? kb.table[(int64_t)b * kb.max_pages + at] : -1;
-  float cc[8], ss[8];
-  const bool turn = !is_value && w < n_rot;
-  if (turn) {
-    const float* cs = a.rot.cos_sin + p * a.rot.dim + 8 * w;
-    load8<false>(cs, cc);
-    load8<false>(cs + (a.rot.dim >> 1), ss);
-  }
-  if (page < 0 || page >= kb.pages.n_pages) {
-    if (u == 0) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
-    return;
-  }
+  // The unit to its place as token i of sequence b.
+  auto append = [&](int b, int i) {
+    const int64_t p = kb.pos[b] + i;
+    if (p < 0 || (rotates && p >= a.rot.max_pos)) {
+      if (u == 0) set_err(kb.dev_err, KDA_DEV_ERR_POS);
+      return;
+    }
+    const int64_t at = p >> kb.page_shift;
+    const int32_t page = at < kb.max_pages ? kb.table[(int64_t)b * kb.max_pages + at] : -1;
+    float cc[8], ss[8];
+    const bool turn = !is_value && w < n_rot;
+    if (turn) {
+      const float* cs = a.rot.cos_sin + p * a.rot.dim + 8 * w;
+      load8<false>(cs, cc);
+      load8<false>(cs + (a.rot.dim >> 1), ss);
+    }
+    if (page < 0 || page >= kb.pages.n_pages) {
+      if (u == 0) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
+      return;
+    }
 
-  if (turn) {
-    if (a.rot.pairs) {
-      // x holds pairs 0..3 interleaved, y pairs 4..7.
+    if (turn) {
+      if (a.rot.pairs) {
+        // x holds pairs 0..3 interleaved, y pairs 4..7.
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float x0 = x[2 * n], x1 = x[2 * n + 1], y0 = y[2 * n], y1 = y[2 * n + 1];
-        x[2 * n] = x0 * cc[n] - x1 * ss[n];
-        x[2 * n + 1] = x1 * cc[n] + x0 * ss[n];
-        y[2 * n] = y0 * cc[4 + n] - y1 * ss[4 + n];
-        y[2 * n + 1] = y1 * cc[4 + n] + y0 * ss[4 + n];
-      }
-    } else {
+        for (int n = 0; n < 4; ++n) {
+          const float x0 = x[2 * n], x1 = x[2 * n + 1], y0 = y[2 * n], y1 = y[2 * n + 1];
+          x[2 * n] = x0 * cc[n] - x1 * ss[n];
+          x[2 * n + 1] = x1 * cc[n] + x0 * ss[n];
+          y[2 * n] = y0 * cc[4 + n] - y1 * ss[4 + n];
+          y[2 * n + 1] = y1 * cc[4 + n] + y0 * ss[4 + n];
+        }
+      } else {
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const float x0 = x[n], y0 = y[n];
-        x[n] = x0 * cc[n] - y0 * ss[n];
-        y[n] = y0 * cc[n] + x0 * ss[n];
+        for (int n = 0; n < 8; ++n) {
+          const float x0 = x[n], y0 = y[n];
+          x[n] = x0 * cc[n] - y0 * ss[n];
+          y[n] = y0 * cc[n] + x0 * ss[n];
+        }
       }
     }
-  }
-  if (!is_value && !is_key) {
-    TIn* dst = static_cast<TIn*>(a.q_out) + row * a.q_out_stride + h * DK;
-    store8<NT>(dst + c0, x);
-    store8<NT>(dst + c1, y);
-    return;
-  }
-  const int64_t place = (((int64_t)page * kb.s.Hkv + h) << kb.page_shift) + ((int)p & (kb.pages.page_size - 1));
-  TC* dst = is_value ? static_cast<TC*>(kb.pages.v) + place * DV : static_cast<TC*>(kb.pages.k) + place * DK;
-  if constexpr (kE4m3) {
-    const float scale = (is_value ? kb.pages.v_scale : kb.pages.k_scale)[h];
-    store8_e4m3<NT>(dst + c0, x, scale);
-    store8_e4m3<NT>(dst + c1, y, scale);
-  } else {
-    store8<NT>(dst + c0, x);
-    store8<NT>(dst + c1, y);
+    if (!is_value && !is_key) {
+      TIn* dst = static_cast<TIn*>(a.q_out) + row * a.q_out_stride + h * DK;
+      store8<NT>(dst + c0, x);
+      store8<NT>(dst + c1, y);
+      return;
+    }
+    const int64_t place = (((int64_t)page * kb.s.Hkv + h) << kb.page_shift) + ((int)p & (kb.pages.page_size - 1));
+    TC* dst = is_value ? static_cast<TC*>(kb.pages.v) + place * DV : static_cast<TC*>(kb.pages.k) + place * DK;
+    if constexpr (kE4m3) {
+      const float scale = (is_value ? kb.pages.v_scale : kb.pages.k_scale)[h];
+      store8_e4m3<NT>(dst + c0, x, scale);
+      store8_e4m3<NT>(dst + c1, y, scale);
+    } else {
+      store8<NT>(dst + c0, x);
+      store8<NT>(dst + c1, y);
+    }
+  };
+  // A second turn only for a key or value that several ranges hold: one of them
+  // begins before a range that runs backwards.
+  for (int from = 0;;) {
+    load8<NT>(src + c0, x);
+    load8<NT>(src + c1, y);
+    Owner o;
+    if (kb.tok_start)
+      o = owner_of(kb, row, from);
+    else
+      o.b = row / kb.s.T, o.token = row - o.b * kb.s.T, o.more = false;
+    if (live && o.b >= 0) append(o.b, o.token);
+    const bool again = o.more && (is_key || is_value);
+    if (__ballot(again) == 0) break;
+    from = again ? o.b + 1 : kb.s.B;
   }
 }
 

@@ -86,3 +86,50 @@ def run_ranges(kda, form, hq, hkv, starts, N, T, seed, pairs=False):
 def test_rows_before_the_first_sequence(kda, form, hq, hkv, starts, N, T):
     """A wave that begins in rows of no sequence still serves the rows that follow."""
     assert run_ranges(kda, form, hq, hkv, starts, N, T, seed=41) == 0
+
+
+@pytest.mark.parametrize("form,hq,hkv", [("bf16_d64", 2, 2), ("f32_d64", 1, 1), ("e4m3_d128", 4, 2), ("latent", 16, 1)])
+@pytest.mark.parametrize("starts,N,T", [([0, 3, 4, 4, 7, 25, 10, 13, 17, 17, 20], 20, 4), ([0, 1000, 1000, 6, 9], 9, 3),
+                                        ([-2, 1, 3, 5], 5, 2), ([2, 0, 2, 4], 4, 2), ([0, 2, -1000, 4, 6], 6, 2),
+                                        ([0, 9, 9, 12, 14], 14, 3)])
+def test_a_bad_range_takes_nothing_from_the_others(kda, form, hq, hkv, starts, N, T):
+    assert run_ranges(kda, form, hq, hkv, starts, N, T, seed=42) == 128
+
+
+@pytest.mark.parametrize("form,hq,hkv", [("bf16_d64", 2, 1), ("latent", 2, 1)])
+@pytest.mark.parametrize("at,to", [(63, 10 ** 6), (64, 10 ** 6), (63, -7), (1, 2 ** 31 - 1), (1, -2 ** 31), (129, 10 ** 6),
+                                   (0, 10 ** 6), (100, 0)])
+def test_a_bad_range_among_many_sequences(kda, form, hq, hkv, at, to):
+    """One entry changed in a list of 130 sequences, idle ones among them."""
+    counts = np.random.default_rng(1).integers(0, 4, 130)
+    counts[[0, 62, 63, 64, 99, 100, 128, 129]] = 2
+    starts = [0, *np.cumsum(counts).tolist()]
+    N = starts[-1]
+    starts[at] = to
+    assert run_ranges(kda, form, hq, hkv, starts, N, 3, seed=43) == 128
+
+
+@pytest.mark.parametrize("form,hq,hkv", [("bf16_d64", 2, 2), ("e4m3_d128", 2, 1), ("latent", 8, 1)])
+@pytest.mark.parametrize("starts,N,T", [([0, 3, 1, 4], 4, 3), ([0, 4, 0, 4, 0, 4], 4, 4), ([1, 3, 2, 4, 3, 6], 7, 3)])
+def test_ranges_that_overlap(kda, form, hq, hkv, starts, N, T):
+    """Each sequence's tokens reach its own pages, also from a row that a second sequence's range holds."""
+    assert run_ranges(kda, form, hq, hkv, starts, N, T, seed=44) == 128
+
+
+def test_many_sequences_with_gaps(kda):
+    """Sequences of one token among idle ones, with rows of no sequence in front and behind."""
+    counts = np.random.default_rng(2).integers(0, 2, 300)
+    starts = [9, *(9 + np.cumsum(counts)).tolist()]
+    assert run_ranges(kda, "bf16_d64", 1, 1, starts, starts[-1] + 20, 1, seed=45) == 0
+
+
+@pytest.mark.parametrize("at", [2, 255, 256, 257, 511, 512, 513, 598])
+@pytest.mark.parametrize("back", [10 ** 6, 2])
+def test_a_bad_range_among_hundreds(kda, at, back):
+    """Lists that are read 256 ranges at a time, and the rest: one entry far off, or one that reaches back over the
+    rows of sequences before (a sequence without tokens between them runs backwards)."""
+    counts = np.random.default_rng(3).integers(0, 4, 600)
+    counts[[at - 2, at - 1, at]] = 2, 0, 2
+    starts = [0, *np.cumsum(counts).tolist()]
+    starts[at] = starts[at] + back if back > 5 else starts[at] - back
+    assert run_ranges(kda, "bf16_d64", 2, 1, starts, int(counts.sum()), 5, seed=46) == 128
