@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(kWaves * kWave, 2) latent_kernel(AttnArgs a) {
           }
         }
         auto weights = [&](int n) { return __builtin_bit_cast(bf16x8, lds_p[i & 1][n][lane]); };
-        bf16x8 w[2] = {weights(0), weights(1)};
+        bf16x8 w[2] = {weights(0), bf16x8{}};
+        if constexpr (RB > 1) w[1] = weights(1);
 #pragma unroll
         for (int n = 0; n < RB; ++n) {
           __builtin_amdgcn_sched_barrier(0);
