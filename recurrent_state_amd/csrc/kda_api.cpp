@@ -155,9 +155,6 @@ kda_status check_kv(const kda_kv_shape* s, const kda_pages* pages, const int32_t
   if (r != KDA_OK) return r;
   if (n_tokens < 0 || n_tokens > 1 << 30) return KDA_ERR_SHAPE;
   if (!tok_start && (int64_t)n_tokens != (int64_t)s->B * s->T) return KDA_ERR_SHAPE;
-  // A thread to each unit of 16 values, and a launch has below 2^32 of them.
-  const int64_t units = ((int64_t)s->Hq * s->dk + (int64_t)s->Hkv * (s->dk + s->dv)) / 16;
-  if ((int64_t)n_tokens * units > ((int64_t)1 << 32) - 256) return KDA_ERR_SHAPE;
   if (s->B > 0 && n_tokens > 0) {
     const bool latent = is_latent(*s);
     if (pages->n_pages < 1) return KDA_ERR_SHAPE;
@@ -672,6 +669,9 @@ kda_status kda_kv_append(const kda_kv_shape* shape, const kda_pages* pages, cons
   if (r != KDA_OK) return r;
   const kda_kv_shape& s = *shape;
   const bool latent = is_latent(s);
+  // A thread to each unit of 16 values, and a launch has below 2^32 of them.
+  const int64_t units = ((int64_t)s.Hq * s.dk + (int64_t)s.Hkv * (s.dk + s.dv)) / 16;
+  if ((int64_t)n_tokens * units > ((int64_t)1 << 32) - 256) return KDA_ERR_SHAPE;
   if (rot) {
     if (rot->max_pos < 1 || rot->dim < 16 || rot->dim % 16 != 0 || rot->start < 0 || rot->start % 16 != 0 ||
         (int64_t)rot->start + rot->dim > s.dk)
