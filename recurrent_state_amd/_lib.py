@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch  # loads the HIP runtime that libkda then shares (same soname)
 
@@ -880,6 +881,17 @@ def attn_workspace(pool: PagePool, table, *, Hq: int, T: int = 1):
     return torch.empty(n, dtype=torch.uint8, device=pool.device)
 
 
+def _attn_scale(pool: PagePool, scale):
+    """A call's scale: the keys' width ** -0.5 where none is given."""
+    if scale is not None:
+        return float(scale)
+    if pool.latent:
+        # Not an error: latent calls without a scale have always had this one.
+        warnings.warn(f"a latent cache's keys are {pool.dk} wide, but its model's scale is that of the width before "
+                      f"the up-projection was absorbed: pass scale ({pool.dk} ** -0.5 is used)", stacklevel=3)
+    return float(pool.dk) ** -0.5
+
+
 class AttnDecodePlan:
     """An attn_decode call validated once (see DecodePlan)."""
 
@@ -898,8 +910,8 @@ class AttnDecodePlan:
         self._keep = (pool, table, pos, q, o, workspace, lse, tok_start, dev_err, sh)
         self._device = dev
         self._args = (ctypes.byref(sh), ctypes.byref(pool.c), _ptr(table), table.shape[1], _ptr(tok_start), N,
-                      _ptr(pos), _ptr(q), qs, float(pool.dk) ** -0.5 if scale is None else float(scale), int(window),
-                      _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(dev_err))
+                      _ptr(pos), _ptr(q), qs, _attn_scale(pool, scale), int(window), _ptr(o), _ptr(lse),
+                      _ptr(workspace), workspace.numel(), _ptr(dev_err))
         self._fn = lib().kda_attn_decode
 
     def __call__(self):
@@ -911,6 +923,9 @@ def attn_decode(pool: PagePool, table, pos, q, o, workspace, dev_err, **kw):
 
     q, o: [B][T][Hq][width], or packed [N][Hq][width] with tok_start and T;
     lse (optional): f32, o's shape without the width.  window: the tokens that a
-    query sees (0: all).  Keywords: lse, scale, window, tok_start, T.
+    query sees (0: all).  scale: of the scores, the pool's dk ** -0.5 if left
+    out; a latent pool's should be given, since its keys are wider than those
+    that the model trained with (a warning says so).  Keywords: lse, scale,
+    window, tok_start, T.
     """
     AttnDecodePlan(pool, table, pos, q, o, workspace, dev_err, **kw)()
