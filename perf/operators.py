@@ -204,7 +204,7 @@ def prepare(case, seed):
             s["lse"] = torch.empty((N, Hq), device=DEV, dtype=torch.float32)
             ws = kda.attn_workspace(s["pool"], s["table"], Hq=Hq, T=T)
             s["call"] = kda.AttnDecodePlan(s["pool"], s["table"], s["pos"], s["q"], s["o"], ws, err, lse=s["lse"],
-                                           window=case["window"], tok_start=s["tok_start"], T=T)
+                                           scale=dk ** -0.5, window=case["window"], tok_start=s["tok_start"], T=T)
     return s
 
 
