@@ -65,7 +65,7 @@ def run_ranges(kda, form, hq, hkv, starts, N, T, seed, pairs=False):
     # The same ranges read back.
     o, lse = torch.full((N, hq, b.dv), 7.0, dtype=b.dt, device="cuda"), torch.full((N, hq), 7.0, device="cuda")
     ws = kda.attn_workspace(pool, b.table, Hq=hq, T=T)
-    kda.attn_decode(pool, b.table, b.pos, q, o, ws, b.err, lse=lse, tok_start=ts, T=T)
+    kda.attn_decode(pool, b.table, b.pos, q, o, ws, b.err, lse=lse, scale=b.dk ** -0.5, tok_start=ts, T=T)
     torch.cuda.synchronize()
     for s, r0, n in seqs:
         rows = [r for r in range(r0, r0 + n) if owned[r] == 1]
