@@ -529,9 +529,10 @@ kda_status kda_mixed_step(const kda_shape* shape, const int32_t* roles, const in
  * pos[b] + i.  A range that is outside [0, n_tokens], runs backwards or is
  * longer than T sets KDA_DEV_ERR_TOKENS in *dev_err and the sequence is
  * skipped (nothing of it is written); every other sequence is served by its
- * own range.  (Such ranges overlap only where one between them runs backwards:
- * q_out, o and lse of a row that several hold are those of any of them.)  Rows
- * of no sequence, before, between or behind the others, are left as they are.
+ * own range.  (Ranges overlap only where one between them runs backwards: each
+ * sequence's pages then get its tokens, and what q_out, o and lse hold in a row
+ * of several sequences is not specified.)  Rows of no sequence, before, between
+ * or behind the others, are left as they are.
  */
 typedef struct kda_kv_shape {
   int32_t B;           /* sequences in the batch */
