@@ -73,14 +73,6 @@ __device__ __forceinline__ float max_over_rows(float x) {
 
 // A value that every lane holds, moved to a scalar register.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-// x, as a value that the compiler knows nothing of: what is computed from it
-// stays where it is used, instead of being hoisted out of the loops around
-// and held in registers (or spilled) for all of them.
-__device__ __forceinline__ int here(int x) {
-  asm volatile("" : "+v"(x));
-  return x;
-}
-
 // A sequence's part in the call: rows row0 .. row0 + n - 1, its visible tokens
 // [lo, end) of all its rows together, and its tiles (of TILE tokens, from the
 // one that holds lo).  A sequence whose rows all come before its first token

@@ -11,6 +11,14 @@ namespace {
 
 __device__ __forceinline__ void set_err(int32_t* dev_err, int32_t bit) { atomicOr(dev_err, bit); }
 
+// x, as a value that the compiler knows nothing of: what is computed from it
+// stays where it is used, instead of being hoisted out of the loops around
+// and held in registers (or spilled) for all of them.
+__device__ __forceinline__ int here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // The new tokens of sequence b: packed rows row0 .. row0 + n - 1.  n = 0 for a
 // sequence that sits the call out; bad: its range does not fit the launch.
 struct SeqRows {
