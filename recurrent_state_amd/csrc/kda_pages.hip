@@ -196,7 +196,7 @@ __device__ __forceinline__ int append_unit(const AppendArgs& a, uint32_t e, int 
   auto append = [&] {
     const int64_t p = kb.pos[b] + o.token;
     if (p < 0 || (rotates && p >= a.rot.max_pos)) {
-      if (u == 0) set_err(kb.dev_err, KDA_DEV_ERR_POS);
+      if (u == a.units_q) set_err(kb.dev_err, KDA_DEV_ERR_POS);
       return;
     }
     const int64_t at = p >> kb.page_shift;
@@ -209,7 +209,7 @@ __device__ __forceinline__ int append_unit(const AppendArgs& a, uint32_t e, int 
       load8<false>(cs + (a.rot.dim >> 1), ss);
     }
     if (page < 0 || page >= kb.pages.n_pages) {
-      if (u == 0) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
+      if (u == a.units_q) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
       return;
     }
 

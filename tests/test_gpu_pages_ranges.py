@@ -133,3 +133,21 @@ def test_a_bad_range_among_hundreds(kda, at, back):
     starts = [0, *np.cumsum(counts).tolist()]
     starts[at] = starts[at] + back if back > 5 else starts[at] - back
     assert run_ranges(kda, "bf16_d64", 2, 1, starts, int(counts.sum()), 5, seed=46) == 128
+
+
+@pytest.mark.parametrize("what,bit", [("page", 32), ("pos", 64)])
+def test_errors_of_a_second_sequence_are_named(kda, what, bit):
+    """A row's second sequence has its own position and pages, and its own errors."""
+    b = Batch("bf16_d64", Hq=2, Hkv=1, page=16, pos=[4, 0, 9], counts=[3, 3, 3], seed=47)
+    q, k, v = (x[:4].contiguous() for x in (b.q, b.k, b.v))
+    if what == "page":
+        b.table[2] = -1
+    else:
+        b.pos[2] = -3
+    ts = torch.tensor([0, 3, 1, 3], dtype=torch.int32, device="cuda")      # sequence 2's rows are sequence 0's
+    kp = f64(b.k_pages)
+    po.append(kp, f64(b.v_pages), b.np_table()[:1], np.array([4]), [3], f64(k[:3]), f64(v[:3]), f64(q[:3]), f64(b.cos_sin))
+    kda.kv_append(b.pool(kda), b.table, b.pos, k, v, b.err, q=q, q_out=torch.empty_like(q), cos_sin=b.cos_sin, tok_start=ts,
+                  T=3)
+    assert b.err.item() == 128 | bit
+    check_rows(b.k_pages, kp, b.ct, 2 * float(k.float().abs().max()))
