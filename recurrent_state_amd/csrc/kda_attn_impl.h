@@ -426,7 +426,9 @@ __global__ void __launch_bounds__(DV / 4 * kJoinGroups<DV>) join_kernel(AttnArgs
   }
 }
 
-// Whether the pool is larger than the 256 MB that the memory side caches.
+// Whether the pool is larger than the 256 MB that the memory side caches.  (How
+// much of it a call reads is known on the device only: a short window in a large
+// pool counts as the pool.)
 inline bool outgrows_cache(const KvBatch& kb) {
   const int64_t es = kb.s.cache_dtype == KDA_F32 ? 4 : kb.s.cache_dtype == KDA_BF16 ? 2 : 1;
   const int64_t row = kb.pages.v ? kb.s.dk + kb.s.dv : kb.s.dk;

@@ -11,9 +11,11 @@
 //
 // Bound by memory for prompts, and by the chain of dependent loads (token range,
 // position, page) for a few tokens: the unit's values depend on none of these
-// and are asked for first.  Measured, 32 query and 8 kv heads of 128 in bf16:
-// eight prompts of 8192 tokens 290 us (1.64 GB, 5.7 TB/s), one token 2.6 us;
-// 256 tokens of a latent cache 6.5 us.
+// and are asked for first.  Measured, the kernel by itself, 32 query and 8 kv
+// heads of 128: eight prompts of 8192 tokens in bf16 285 us (1.64 GB, 5.8 TB/s),
+// into e4m3 286 (5.3 TB/s), four in f32 338 (4.8 TB/s), four latent ones 504
+// (2.50 GB, 5.0 TB/s); one token 2.6 us, 256 tokens of a latent cache 6.6 us.  A
+// call of one token among others takes 4.2 us, which is the host's part.
 
 #include "kda_pages.h"
 
@@ -273,8 +275,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
 }
 
 // Calls that touch more than the 256 MB Infinity Cache go past it: 65536 tokens
-// of 32 + 8 heads of 128 in 319 -> 290 us.  What smaller calls write stays there
-// for the attention that reads it next.
+// of 32 + 8 heads of 128 in 284 us for 288 with plain accesses, into e4m3 285 for
+// 303.  f32 and latent prompts lose by it (16384 f32 tokens 170 us for 147, 32768
+// latent ones 503 for 444).  What smaller calls write stays there for the
+// attention that reads it next.
 template <int DK, int DV, typename TIn, typename TC>
 hipError_t run(const AppendArgs& a, hipStream_t st) {
   const int64_t units = (int64_t)a.kb.n_tokens * a.units, blocks = (units + kThreads - 1) / kThreads;
