@@ -107,12 +107,13 @@ struct Owner {
   int b, token;
   bool more;  // a later sequence's range holds the row too
 };
-// The first such sequence from `from` on.  Every range counts by itself, so that
-// one that does not fit the launch takes nothing from the others, wherever its
-// ends point.  All of them are looked at, a lane taking four of 256 neighbours
-// (the rest 64 at a time), and the few that meet the wave's rows, which ascend
-// with the lanes, are held against each lane's.
-__device__ __forceinline__ Owner owner_of(const KvBatch& kb, int row, int from) {
+// The first such sequence from `from` on (`begin`: the wave's smallest, or less).
+// Every range counts by itself, so that one that does not fit the launch takes
+// nothing from the others, wherever its ends point.  They are looked at until
+// every lane that looks has met two: a lane takes four of 256 neighbours (the rest
+// 64 at a time), and the few that meet the wave's rows, which ascend with the
+// lanes, are held against each lane's.
+__device__ __forceinline__ Owner owner_of(const KvBatch& kb, int row, int from, int begin) {
   const int lane = here((int)threadIdx.x & 63), B = kb.s.B;
   const int first = __builtin_amdgcn_readfirstlane(row), last = __builtin_amdgcn_readlane(row, kWave - 1);
   Owner o{-1, 0, false};
@@ -125,7 +126,7 @@ __device__ __forceinline__ Owner owner_of(const KvBatch& kb, int row, int from) 
       if (o.b < 0 || b < o.b) o.b = b, o.token = row - r0;
     }
   };
-  int c = 0;
+  int c = begin & ~(4 * kWave - 1);
   for (; c + 4 * kWave <= B; c += 4 * kWave) {
     const int32_t* p = kb.tok_start + c + 4 * lane;
     int32_t at[5];
@@ -137,6 +138,7 @@ __device__ __forceinline__ Owner owner_of(const KvBatch& kb, int row, int from) 
     if (__ballot(any) == 0) continue;
 #pragma unroll
     for (int j = 0; j < 4; ++j) meet(c + j, 4, at[j], at[j + 1]);
+    if (__ballot(from < B && !o.more) == 0) return o;
   }
   for (; c < B; c += kWave) {
     const int b = min(c + lane, B - 1);
@@ -145,10 +147,11 @@ __device__ __forceinline__ Owner owner_of(const KvBatch& kb, int row, int from) 
   return o;
 }
 
-// Unit e to its place for the first sequence from `from` on that has its row.
+// Unit e to its place for the first sequence from `from` on that has its row
+// (`begin`: see owner_of).
 // Returns where a search for a further one begins, B if there is none.
 template <int DK, int DV, typename TIn, typename TC, bool NT>
-__device__ __forceinline__ int append_unit(const AppendArgs& a, uint32_t e, int from) {
+__device__ __forceinline__ int append_unit(const AppendArgs& a, uint32_t e, int from, int begin) {
   constexpr bool kE4m3 = sizeof(TC) == 1;
   const KvBatch& kb = a.kb;
   // Row and unit of this thread; the threads past the last unit take part in
@@ -191,7 +194,7 @@ __device__ __forceinline__ int append_unit(const AppendArgs& a, uint32_t e, int 
 
   Owner o;
   if (kb.tok_start)
-    o = owner_of(kb, row, from);
+    o = owner_of(kb, row, from, begin);
   else
     o.b = row / kb.s.T, o.token = row - o.b * kb.s.T, o.more = false;
   const int b = o.b, next = o.more && (is_key || is_value) ? b + 1 : kb.s.B;
@@ -268,10 +271,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
   // begins before a range that runs backwards.  here(), also in owner_of: what a
   // turn computes is not kept for the next, which took 20 registers (8 prompts of
   // 8192 tokens to e4m3 364 us, now 285).
-  int from = 0;
-  do
-    from = append_unit<DK, DV, TIn, TC, NT>(a, here((int)(blockIdx.x * kThreads + threadIdx.x)), from);
-  while (__ballot(from < kb.s.B) != 0);
+  for (int from = 0, begin = 0;;) {
+    from = append_unit<DK, DV, TIn, TC, NT>(a, here((int)(blockIdx.x * kThreads + threadIdx.x)), from, begin);
+    if (__ballot(from < kb.s.B) == 0) return;
+    begin = from;
+#pragma unroll
+    for (int i = 1; i < kWave; i *= 2) begin = min(begin, __shfl_xor(begin, i));
+    begin = __builtin_amdgcn_readfirstlane(begin);
+  }
 }
 
 // Calls that touch more than the 256 MB Infinity Cache go past it: 65536 tokens

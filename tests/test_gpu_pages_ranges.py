@@ -151,3 +151,10 @@ def test_errors_of_a_second_sequence_are_named(kda, what, bit):
                   T=3)
     assert b.err.item() == 128 | bit
     check_rows(b.k_pages, kp, b.ct, 2 * float(k.float().abs().max()))
+
+
+@pytest.mark.parametrize("form,hq,hkv", [("bf16_d64", 2, 1), ("latent", 1, 1)])
+def test_rows_of_very_many_sequences(kda, form, hq, hkv):
+    """Ranges forth and back over the same rows: each turn of a row's search goes on where the one before met a
+    sequence."""
+    assert run_ranges(kda, form, hq, hkv, [0, 2] * 1500 + [1, 3], 3, 2, seed=48) == 128
