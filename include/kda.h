@@ -89,8 +89,8 @@ typedef enum kda_dtype {
 #define KDA_DEV_ERR_SLOT_ID 8   /* a device-side state slot id was outside [0, n_slots) */
 #define KDA_DEV_ERR_MIXED 16    /* kda_mixed_step: roles or token ranges inconsistent with the launch */
 #define KDA_DEV_ERR_PAGE 32     /* a page id outside [0, n_pages), or a position past the page table */
-#define KDA_DEV_ERR_POS 64      /* kda_kv_append: a position below 0 or past the rotation table */
-#define KDA_DEV_ERR_TOKENS 128  /* kda_kv_append, kda_attn_decode: a token range inconsistent with the launch */
+#define KDA_DEV_ERR_POS 64      /* appends: a position below 0 or past the rotation table */
+#define KDA_DEV_ERR_TOKENS 128  /* paged attention calls: a token range inconsistent with the launch */
 
 /* Kernel variants reported by kda_last_variant(). */
 #define KDA_VARIANT_NONE 0
@@ -118,6 +118,11 @@ typedef enum kda_dtype {
 #define KDA_VARIANT_MIXED 22
 #define KDA_VARIANT_KV_APPEND 23
 #define KDA_VARIANT_ATTN_DECODE 24
+#define KDA_VARIANT_KV_APPEND_AXES 25
+#define KDA_VARIANT_KV_APPEND_BLOCKS 26
+#define KDA_VARIANT_ATTN_DECODE_BLOCKS 27
+#define KDA_VARIANT_ATTN_WEIGHTS 28
+#define KDA_VARIANT_KV_EVICT 29
 
 /* What a sequence does in a kda_mixed_step. */
 #define KDA_ROLE_IDLE 0    /* nothing this step */
@@ -634,6 +639,151 @@ kda_status kda_attn_decode(const kda_kv_shape* shape, const kda_pages* pages, co
 
 /* Bytes of kda_attn_decode's workspace for calls with up to shape->T new tokens; 0 for an invalid shape. */
 size_t kda_attn_workspace_bytes(const kda_kv_shape* shape, const kda_pages* pages, int32_t max_pages);
+
+/*
+ * Positions of a token on several axes (time, height and width of images and
+ * video, or one axis whose positions are not the places in the cache): pair n
+ * of the rotation turns by the token's position on axis axis_of[n].
+ *   pos      device i64: token row r's position on axis a at pos[a * stride + r]
+ *            (stride 0: n_tokens; rows as those of k)
+ *   n_axes   1 to 4
+ *   axis_of  HOST array of rot->dim / 2 axes, each below n_axes, read during
+ *            the call
+ */
+typedef struct kda_axes {
+  const int64_t* pos;
+  int64_t stride;
+  int32_t n_axes;
+  const uint8_t* axis_of;
+} kda_axes;
+
+/*
+ * kda_kv_append with the rotation's positions from `axes`: the n-th pair of
+ * row r turns by the cosines and sines of cos_sin[axes->pos[axis_of[n]][r]].
+ * The tokens' places in the cache are pos[b] + i as before, and need not fit
+ * the rotation table.  A token with a position outside [0, rot->max_pos) on
+ * any of the axes sets KDA_DEV_ERR_POS and is skipped, as is one whose place
+ * is below 0.  rot and axes must not be NULL.  Otherwise as kda_kv_append; equal
+ * positions on all axes give its bits.
+ */
+kda_status kda_kv_append_axes(const kda_kv_shape* shape, const kda_pages* pages, const int32_t* table,
+                              int32_t max_pages, const int32_t* tok_start, int32_t n_tokens, const int64_t* pos,
+                              const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+                              int64_t q_stride, void* q_out, int64_t q_out_stride, const kda_rotation* rot,
+                              const kda_axes* axes, int32_t* dev_err, void* stream);
+
+/*
+ * Scales of e4m3 pages by blocks of tokens (grouped form, in_dtype KDA_BF16):
+ *   k, v   f32 [n_pages][Hkv][page_size / block]: the page's tokens i * block
+ *          and on hold value / scale with scale i of their kv head
+ *   block  a power of two from 16 to page_size
+ * Calls that take these ignore kda_pages.k_scale and v_scale.  The append sets
+ * a scale to a power of two, so that dividing by it loses nothing.  The
+ * attention takes any scales.
+ */
+typedef struct kda_block_scales {
+  float* k;
+  float* v;
+  int32_t block;
+} kda_block_scales;
+
+/*
+ * Append to pages whose scales go by blocks.  With m the largest finite |value|
+ * that the call puts into a block of a kv head (keys, rotated, and values
+ * apart), the block needs the scale
+ *   2^e, e the least integer with m <= 448 * 2^e, but at least -64.
+ * A block whose first token is new gets that scale.  One that holds earlier
+ * tokens of the sequence (the call begins inside it) gets the larger of that
+ * and its scale so far, rounded up to a power of two; where this raises it, the
+ * earlier tokens are rounded anew, to old * (old scale / new scale), which
+ * changes only values below 2^-6 new scales (the type's subnormals).  New values
+ * are x / scale, clamped to +-448 (infinities too) and rounded to nearest even,
+ * NaN stays NaN.  A scale that rejected drafts raised stays raised while its block
+ * holds tokens from before them.  Tokens of different sequences must not share
+ * a block.  axes NULL: the positions of the rotation are the places, as in
+ * kda_kv_append; otherwise as in kda_kv_append_axes (rot is then required).
+ * Skipped tokens (see kda_kv_append) count for no scale.  Otherwise as
+ * kda_kv_append.
+ */
+kda_status kda_kv_append_blocks(const kda_kv_shape* shape, const kda_pages* pages, const kda_block_scales* scales,
+                                const int32_t* table, int32_t max_pages, const int32_t* tok_start, int32_t n_tokens,
+                                const int64_t* pos, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                                const kda_rotation* rot, const kda_axes* axes, int32_t* dev_err, void* stream);
+
+/*
+ * kda_attn_decode over such pages: k_j and v_j are the stored values times the
+ * scales of their blocks.  Scales of blocks without a visible token do not
+ * matter, whatever they hold.  workspace as kda_attn_workspace_bytes says for
+ * this shape and pool.
+ */
+kda_status kda_attn_decode_blocks(const kda_kv_shape* shape, const kda_pages* pages, const kda_block_scales* scales,
+                                  const int32_t* table, int32_t max_pages, const int32_t* tok_start, int32_t n_tokens,
+                                  const int64_t* pos, const void* q, int64_t q_stride, float scale, int32_t window,
+                                  void* o, float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                  void* stream);
+
+/*
+ * What each cached token is worth to the queries: the attention weights of the
+ * call's query rows, summed by cached token and kv head,
+ *   w[b][h][j] = (j < pos[b] ? w[b][h][j] : 0)
+ *              + sum over the rows r of sequence b that see token j, and the
+ *                query heads of kv head h, of e^(scale (q_r . k_j) - lse_r).
+ * A token's sum thus begins with the call that brings it (appended and attended
+ * to before; those of a prompt that no call weighs begin with what the caller
+ * put there).  Tokens that no row sees are left as they are.
+ *   q, lse   the queries given to kda_attn_decode and the lse that it returned
+ *            (f32 [n_tokens][Hq]), with the same scale and window
+ *   weights  f32 [B][Hkv][weights_stride], weights_stride (floats) at least
+ *            max_pages * page_size
+ * Grouped form; scales NULL: pages as kda_attn_decode, else as
+ * kda_attn_decode_blocks.  1 <= T <= 128 (a decode token, drafts, or the last
+ * tokens of a prompt); otherwise limits as kda_attn_decode.  Every sum is made
+ * in one order: equal calls give equal bits.  Sequences are refused as by
+ * kda_attn_decode, except that a page id outside [0, n_pages) (KDA_DEV_ERR_PAGE)
+ * costs the tokens of that page only.
+ */
+kda_status kda_attn_weights(const kda_kv_shape* shape, const kda_pages* pages, const kda_block_scales* scales,
+                            const int32_t* table, int32_t max_pages, const int32_t* tok_start, int32_t n_tokens,
+                            const int64_t* pos, const void* q, int64_t q_stride, float scale, int32_t window,
+                            const float* lse, float* weights, int64_t weights_stride, int32_t* dev_err, void* stream);
+
+/*
+ * Eviction by those sums.  A sequence b with len[b] cached tokens, more than
+ * `keep`, keeps for each kv head its last `recent` tokens (0 <= recent <= keep)
+ * and, of the others, the keep - recent of the greatest weight (of equal ones
+ * the earlier; -0 equals 0, NaN comes last).  They go, in order, to places
+ * 0 .. keep - 1 of the pages that dst_table lists (device int32
+ * [B][dst_max_pages]); new_len[b] = keep.  The pages that it had are not
+ * changed, so a prefix may be shared.  A sequence of at most `keep` tokens stays
+ * as it is: new_len[b] = len[b], its row of dst_table is not read, and its kept
+ * entries are -1.  Keys keep the rotation of their positions, so later tokens
+ * are appended at places from new_len[b] on with positions of their own (see
+ * kda_axes), and a window counts kept tokens.
+ *   len, new_len   device i64 [B]; may be the same array
+ *   weights        f32 [B][Hkv][weights_stride], as above; finite or not
+ *   new_weights    the same layout: those of the kept tokens (of all tokens of a
+ *                  sequence that stays) at their places, and 0 from new_len[b] on
+ *                  to weights_stride.  Must not overlap weights.
+ *   kept           device int32 [B][Hkv][keep]: the places that the tokens came
+ *                  from, ascending
+ * Destination pages must be pages of this pool that no table row of the call
+ * names as a source, each used once.  With scales, a block's new scale is the
+ * one that kda_kv_append_blocks gives to its values; without, rows are copied
+ * bit for bit (grouped or latent form).  shape gives B, Hkv, dk, dv and
+ * cache_dtype; its T, Hq and in_dtype have to be valid, no more.  keep is at
+ * least 1 and at most dst_max_pages * page_size, weights_stride at least
+ * max_pages * page_size, B * Hkv at most 2^20.  A sequence whose len is below 0
+ * or past its table, or a longer one than keep with a page outside [0, n_pages)
+ * in either table, sets KDA_DEV_ERR_PAGE in *dev_err and is left alone: nothing
+ * of it is moved, new_len[b] = len[b], its kept entries are -1 and its
+ * new_weights 0.
+ */
+kda_status kda_kv_evict(const kda_kv_shape* shape, const kda_pages* pages, const kda_block_scales* scales,
+                        const int32_t* table, int32_t max_pages, const int64_t* len, const float* weights,
+                        int64_t weights_stride, int32_t keep, int32_t recent, const int32_t* dst_table,
+                        int32_t dst_max_pages, int64_t* new_len, float* new_weights, int32_t* kept, int32_t* dev_err,
+                        void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* kda_status_str(kda_status status);

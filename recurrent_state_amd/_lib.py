@@ -24,7 +24,8 @@ VARIANTS = {0: "none", 1: "decode", 2: "verify", 3: "commit", 4: "snapshot", 5: 
             10: "commit_verify_varlen", 11: "decode_prep", 12: "verify_prep", 13: "commit_verify_prep",
             14: "decode_slots", 15: "slot_copy", 16: "prefill_chunked_prep", 17: "prefill_recurrent_prep",
             18: "verify_slots", 19: "commit_slots", 20: "commit_verify_slots", 21: "prefill_chunked_slots",
-            22: "mixed", 23: "kv_append", 24: "attn_decode"}
+            22: "mixed", 23: "kv_append", 24: "attn_decode", 25: "kv_append_axes", 26: "kv_append_blocks",
+            27: "attn_decode_blocks", 28: "attn_weights", 29: "kv_evict"}
 GATE_EXP_NEG_SOFTPLUS, GATE_SIGMOID = 0, 1
 DEV_ERR_ACCEPTED, DEV_ERR_CKPT_SLOT, DEV_ERR_DRAFT_LEN, DEV_ERR_SLOT_ID, DEV_ERR_MIXED = 1, 2, 4, 8, 16
 DEV_ERR_PAGE, DEV_ERR_POS, DEV_ERR_TOKENS = 32, 64, 128
@@ -63,6 +64,15 @@ class _Pages(ctypes.Structure):
 class _Rotation(ctypes.Structure):
     _fields_ = [("cos_sin", ctypes.c_void_p), ("max_pos", ctypes.c_int32), ("start", ctypes.c_int32),
                 ("dim", ctypes.c_int32), ("pairs", ctypes.c_int32)]
+
+
+class _Axes(ctypes.Structure):
+    _fields_ = [("pos", ctypes.c_void_p), ("stride", ctypes.c_int64), ("n_axes", ctypes.c_int32),
+                ("axis_of", ctypes.c_char_p)]
+
+
+class _BlockScales(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block", ctypes.c_int32)]
 
 
 _lib = None
@@ -112,6 +122,17 @@ _SIGS = {
                            _P, _L, ctypes.POINTER(_Rotation), _P, _P]),
     "kda_attn_decode": (_I, [ctypes.POINTER(KvShape), ctypes.POINTER(_Pages), _P, _I, _P, _I, _P, _P, _L,
                              ctypes.c_float, _I, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "kda_kv_append_axes": (_I, [ctypes.POINTER(KvShape), ctypes.POINTER(_Pages), _P, _I, _P, _I, _P, _P, _L, _P, _L, _P,
+                                _L, _P, _L, ctypes.POINTER(_Rotation), ctypes.POINTER(_Axes), _P, _P]),
+    "kda_kv_append_blocks": (_I, [ctypes.POINTER(KvShape), ctypes.POINTER(_Pages), ctypes.POINTER(_BlockScales), _P, _I,
+                                  _P, _I, _P, _P, _L, _P, _L, _P, _L, _P, _L, ctypes.POINTER(_Rotation),
+                                  ctypes.POINTER(_Axes), _P, _P]),
+    "kda_attn_decode_blocks": (_I, [ctypes.POINTER(KvShape), ctypes.POINTER(_Pages), ctypes.POINTER(_BlockScales), _P,
+                                    _I, _P, _I, _P, _P, _L, ctypes.c_float, _I, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "kda_attn_weights": (_I, [ctypes.POINTER(KvShape), ctypes.POINTER(_Pages), ctypes.POINTER(_BlockScales), _P, _I, _P,
+                              _I, _P, _P, _L, ctypes.c_float, _I, _P, _P, _L, _P, _P]),
+    "kda_kv_evict": (_I, [ctypes.POINTER(KvShape), ctypes.POINTER(_Pages), ctypes.POINTER(_BlockScales), _P, _I, _P, _P,
+                          _L, _I, _I, _P, _I, _P, _P, _P, _P, _P]),
     "kda_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(KvShape), ctypes.POINTER(_Pages), _I]),
     "kda_status_str": (ctypes.c_char_p, [_I]),
     "kda_last_variant": (_I, []),
@@ -698,25 +719,34 @@ class PagePool:
 
     `latent` pools have no v: a row's first dv values are its value.  An e4m3
     pool (dtype torch.float8_e4m3fn) holds value / scale, with one f32 scale
-    per kv head in k_scale and v_scale.
+    per kv head in k_scale and v_scale, or, with `scale_block`, one for each
+    scale_block tokens of a page and kv head, f32
+    [n_pages][Hkv][page_size / scale_block], which the appends set.
     """
 
+    c_scales = None  # scales by blocks, for the calls that take them apart from the pages
+
     def __init__(self, n_pages: int, page_size: int, Hkv: int, dk: int, dv: int, device, dtype=torch.bfloat16,
-                 latent: bool = False, k_scale=None, v_scale=None):
+                 latent: bool = False, k_scale=None, v_scale=None, scale_block: int = 0):
+        if scale_block:
+            _check_scale_block(scale_block, page_size, dtype, latent)
+            per = (n_pages, Hkv, page_size // scale_block)
+            k_scale = torch.ones(per, dtype=torch.float32, device=device) if k_scale is None else k_scale
+            v_scale = torch.ones(per, dtype=torch.float32, device=device) if v_scale is None else v_scale
         k = torch.zeros((n_pages, Hkv, page_size, dk), dtype=dtype, device=device)
         v = None if latent else torch.zeros((n_pages, Hkv, page_size, dv), dtype=dtype, device=device)
-        self._hold(k, v, dv, k_scale, v_scale)
+        self._hold(k, v, dv, k_scale, v_scale, scale_block)
 
     @classmethod
-    def from_tensors(cls, k, v=None, *, dv=None, k_scale=None, v_scale=None) -> "PagePool":
+    def from_tensors(cls, k, v=None, *, dv=None, k_scale=None, v_scale=None, scale_block: int = 0) -> "PagePool":
         """A pool over existing tensors (v None: latent, dv its value width)."""
         pool = cls.__new__(cls)
         if v is None and dv is None:
             raise ValueError("a latent pool needs its value width dv")
-        pool._hold(k, v, v.shape[-1] if v is not None else int(dv), k_scale, v_scale)
+        pool._hold(k, v, v.shape[-1] if v is not None else int(dv), k_scale, v_scale, scale_block)
         return pool
 
-    def _hold(self, k, v, dv, k_scale, v_scale):
+    def _hold(self, k, v, dv, k_scale, v_scale, scale_block=0):
         if k.dim() != 4:
             raise ValueError(f"k has shape {tuple(k.shape)}, expected [n_pages][Hkv][page_size][dk]")
         n_pages, Hkv, page_size, dk = k.shape
@@ -726,15 +756,32 @@ class PagePool:
         _need(k, "k", k.shape, k.dtype, k.device)
         if v is not None:
             _need(v, "v", (n_pages, Hkv, page_size, dv), k.dtype, k.device)
+        if scale_block:
+            _check_scale_block(scale_block, page_size, k.dtype, v is None)
         if k.dtype == torch.float8_e4m3fn:
-            _need(k_scale, "k_scale", (Hkv,), torch.float32, k.device)
-            _need(v_scale, "v_scale", (Hkv,), torch.float32, k.device)
+            per = (n_pages, Hkv, page_size // scale_block) if scale_block else (Hkv,)
+            _need(k_scale, "k_scale", per, torch.float32, k.device)
+            _need(v_scale, "v_scale", per, torch.float32, k.device)
         elif k_scale is not None or v_scale is not None:
             raise ValueError("scales belong to float8_e4m3fn pages only")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.Hkv, self.page_size, self.dk = n_pages, Hkv, page_size, dk
-        self.dv, self.latent, self.device = dv, v is None, k.device
+        self.dv, self.latent, self.device, self.scale_block = dv, v is None, k.device, int(scale_block)
         self.c = _Pages(*(None if x is None else x.data_ptr() for x in (k, v, k_scale, v_scale)), n_pages, page_size)
+        if scale_block:
+            self.c_scales = _BlockScales(k_scale.data_ptr(), v_scale.data_ptr(), scale_block)
+
+def _scales(pool):
+    """A call's kda_block_scales: None for a pool without scales by blocks."""
+    c = getattr(pool, "c_scales", None)
+    return None if c is None else ctypes.byref(c)
+
+
+def _check_scale_block(block, page_size, dtype, latent):
+    if dtype != torch.float8_e4m3fn or latent:
+        raise ValueError("scales by blocks belong to float8_e4m3fn pages of keys and values")
+    if block < 16 or block > page_size or block & (block - 1):
+        raise ValueError(f"scale_block is {block}, expected a power of two from 16 to the page size")
 
 
 def _need_gpu(t, name):
@@ -814,11 +861,38 @@ def _packed_T(t, tok_start, T, name):
     return int(T)
 
 
+def rotation_axes(sections, interleaved: bool = False):
+    """The axis of each rotated pair, for kv_append's axis_of: sections[a] pairs turn by axis a, section after section,
+    or, interleaved, dealt to the axes in turn while each one's section lasts."""
+    sections = [int(n) for n in sections]
+    if not 1 <= len(sections) <= 4 or any(n < 0 for n in sections):
+        raise ValueError("sections are the pairs of one to four axes")
+    if not interleaved:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    return [a for i in range(max(sections)) for a, n in enumerate(sections) if i < n]
+
+
+def _axes(axis_pos, axis_of, rot, sh, N, device, tok_start):
+    """kda_axes of an append: axis_pos int64 [axes][B][T] (packed rows: [axes][N])."""
+    if rot is None:
+        raise ValueError("positions on axes need cos_sin")
+    if not isinstance(axis_pos, torch.Tensor):
+        raise TypeError("axis_pos must be a torch.Tensor")
+    A = axis_pos.shape[0] if axis_pos.dim() else 0
+    _need(axis_pos, "axis_pos", (A, N) if tok_start is not None else (A, sh.B, sh.T), torch.int64, device)
+    of = [0] * (rot.dim // 2) if axis_of is None and A == 1 else axis_of
+    if of is None or len(of) != rot.dim // 2:
+        raise ValueError(f"axis_of names the axis of each of the {rot.dim // 2} rotated pairs")
+    if not 1 <= A <= 4 or any(not 0 <= int(a) < A for a in of):
+        raise ValueError("one to four axes, and axis_of below their number")
+    return _Axes(axis_pos.data_ptr(), N, A, bytes(int(a) for a in of))
+
+
 class KvAppendPlan:
     """A kv_append call validated once (see DecodePlan)."""
 
     def __init__(self, pool: PagePool, table, pos, k, v, dev_err, *, q=None, q_out=None, cos_sin=None, rot_start=0,
-                 rot_pairs=False, tok_start=None, T=None):
+                 rot_pairs=False, axis_pos=None, axis_of=None, tok_start=None, T=None):
         dev, dt = pool.device, k.dtype
         T = _packed_T(k, tok_start, T, "k")
         sh = _kv_shape(pool, table, pos, 1 if q is None else q.shape[-2], T, dt, tok_start)
@@ -848,12 +922,18 @@ class KvAppendPlan:
                 raise ValueError(f"cos_sin has shape {tuple(cos_sin.shape)}, expected [max_pos][rotated values]")
             _need(cos_sin, "cos_sin", cos_sin.shape, torch.float32, dev)
             rot = _Rotation(cos_sin.data_ptr(), cos_sin.shape[0], int(rot_start), cos_sin.shape[1], int(rot_pairs))
-        self._keep = (pool, table, pos, k, v, q, q_out, cos_sin, tok_start, dev_err, sh, rot)
+        axes = None if axis_pos is None else _axes(axis_pos, axis_of, rot, sh, N, dev, tok_start)
+        if axes is None and axis_of is not None:
+            raise ValueError("axis_of needs axis_pos")
+        self._keep = (pool, table, pos, k, v, q, q_out, cos_sin, axis_pos, tok_start, dev_err, sh, rot, axes)
         self._device = dev
-        self._args = (ctypes.byref(sh), ctypes.byref(pool.c), _ptr(table), table.shape[1], _ptr(tok_start), N,
-                      _ptr(pos), _ptr(k), ks, _ptr(v), vs, _ptr(q), qs, _ptr(q_out), qos,
-                      None if rot is None else ctypes.byref(rot), _ptr(dev_err))
-        self._fn = lib().kda_kv_append
+        scales = _scales(pool)
+        by_ref = [None if x is None else ctypes.byref(x) for x in (rot, axes)]
+        self._args = (ctypes.byref(sh), ctypes.byref(pool.c), *(() if scales is None else (scales,)), _ptr(table),
+                      table.shape[1], _ptr(tok_start), N, _ptr(pos), _ptr(k), ks, _ptr(v), vs, _ptr(q), qs,
+                      _ptr(q_out), qos, *(by_ref[:1] if scales is None and axes is None else by_ref), _ptr(dev_err))
+        self._fn = (lib().kda_kv_append_blocks if scales is not None else
+                    lib().kda_kv_append if axes is None else lib().kda_kv_append_axes)
 
     def __call__(self):
         _launch_on(self._device, self._fn, self._args)
@@ -866,8 +946,12 @@ def kv_append(pool: PagePool, table, pos, k, v, dev_err, **kw):
     (device int32 [B + 1]) and T, the most tokens of a sequence; they may be
     slices of one projection.  cos_sin: f32 [max_pos][rotated values], cosines
     then sines, rotating the values from rot_start on (rot_pairs: neighbours
-    form the pairs, else halves).  Keywords: q, q_out, cos_sin, rot_start,
-    rot_pairs, tok_start, T.
+    form the pairs, else halves).  axis_pos: int64 [axes][B][T] ([axes][N]),
+    positions for the rotation apart from the places in the cache, of which
+    axis_of (see rotation_axes) names one for each pair; one axis needs no
+    axis_of.  A pool with scale_block gets the scales that the values need.
+    Keywords: q, q_out, cos_sin, rot_start, rot_pairs, axis_pos, axis_of,
+    tok_start, T.
     """
     KvAppendPlan(pool, table, pos, k, v, dev_err, **kw)()
 
@@ -909,10 +993,11 @@ class AttnDecodePlan:
         _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
         self._keep = (pool, table, pos, q, o, workspace, lse, tok_start, dev_err, sh)
         self._device = dev
-        self._args = (ctypes.byref(sh), ctypes.byref(pool.c), _ptr(table), table.shape[1], _ptr(tok_start), N,
-                      _ptr(pos), _ptr(q), qs, _attn_scale(pool, scale), int(window), _ptr(o), _ptr(lse),
-                      _ptr(workspace), workspace.numel(), _ptr(dev_err))
-        self._fn = lib().kda_attn_decode
+        scales = _scales(pool)
+        self._args = (ctypes.byref(sh), ctypes.byref(pool.c), *(() if scales is None else (scales,)), _ptr(table),
+                      table.shape[1], _ptr(tok_start), N, _ptr(pos), _ptr(q), qs, _attn_scale(pool, scale),
+                      int(window), _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(dev_err))
+        self._fn = lib().kda_attn_decode if scales is None else lib().kda_attn_decode_blocks
 
     def __call__(self):
         _launch_on(self._device, self._fn, self._args)
@@ -929,3 +1014,92 @@ def attn_decode(pool: PagePool, table, pos, q, o, workspace, dev_err, **kw):
     window, tok_start, T.
     """
     AttnDecodePlan(pool, table, pos, q, o, workspace, dev_err, **kw)()
+
+
+def _need_weights(weights, name, pool, table):
+    """Sums of weights f32 [B][Hkv][places], at least the table's; the stride of a row in floats."""
+    if not isinstance(weights, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    B, places = table.shape[0], table.shape[1] * pool.page_size
+    if weights.dim() != 3 or tuple(weights.shape[:2]) != (B, pool.Hkv) or weights.shape[2] < places:
+        raise ValueError(f"{name} has shape {tuple(weights.shape)}, expected [{B}][{pool.Hkv}][{places} or more]")
+    _need(weights, name, weights.shape, torch.float32, pool.device)
+    return weights.shape[2]
+
+
+class AttnWeightsPlan:
+    """An attn_weights call validated once (see DecodePlan)."""
+
+    def __init__(self, pool: PagePool, table, pos, q, lse, weights, dev_err, *, scale=None, window=0, tok_start=None,
+                 T=None):
+        dev, dt = pool.device, q.dtype
+        T = _packed_T(q, tok_start, T, "q")
+        sh = _kv_shape(pool, table, pos, q.shape[-2], T, dt, tok_start)
+        Hq, N, qs = _rows(q, "q", sh.B, T, pool.dk, dt, dev, tok_start)
+        _need(lse, "lse", ((N,) if tok_start is not None else (sh.B, T)) + (Hq,), torch.float32, dev)
+        stride = _need_weights(weights, "weights", pool, table)
+        _need(dev_err, "dev_err", (1,), torch.int32, dev)
+        self._keep = (pool, table, pos, q, lse, weights, tok_start, dev_err, sh)
+        self._device = dev
+        scales = _scales(pool)
+        self._args = (ctypes.byref(sh), ctypes.byref(pool.c), scales, _ptr(table), table.shape[1], _ptr(tok_start), N,
+                      _ptr(pos), _ptr(q), qs, _attn_scale(pool, scale), int(window), _ptr(lse), _ptr(weights), stride,
+                      _ptr(dev_err))
+        self._fn = lib().kda_attn_weights
+
+    def __call__(self):
+        _launch_on(self._device, self._fn, self._args)
+
+
+def attn_weights(pool: PagePool, table, pos, q, lse, weights, dev_err, **kw):
+    """Adds the attention weights of the new tokens' queries to each cached token's sum.
+
+    q, scale and window as given to attn_decode, lse as it returned it; weights:
+    f32 [B][Hkv][places], summed over the rows and the query heads of a kv head.
+    A new token's own sum begins with this call.  Keywords: scale, window,
+    tok_start, T.
+    """
+    AttnWeightsPlan(pool, table, pos, q, lse, weights, dev_err, **kw)()
+
+
+class KvEvictPlan:
+    """A kv_evict call validated once (see DecodePlan)."""
+
+    def __init__(self, pool: PagePool, table, length, weights, dst_table, new_length, new_weights, kept, dev_err, *,
+                 recent=0):
+        dev = pool.device
+        sh = _kv_shape(pool, table, length, pool.Hkv, 1,
+                       torch.float32 if pool.k.dtype == torch.float32 else torch.bfloat16, None)
+        if dst_table.dim() != 2:
+            raise ValueError(f"dst_table has shape {tuple(dst_table.shape)}, expected [B][pages]")
+        _need(dst_table, "dst_table", (sh.B, dst_table.shape[1]), torch.int32, dev)
+        _need(new_length, "new_length", (sh.B,), torch.int64, dev)
+        stride = _need_weights(weights, "weights", pool, table)
+        _need(new_weights, "new_weights", weights.shape, torch.float32, dev)
+        if kept.dim() != 3:
+            raise ValueError(f"kept has shape {tuple(kept.shape)}, expected [B][Hkv][tokens to keep]")
+        _need(kept, "kept", (sh.B, pool.Hkv, kept.shape[2]), torch.int32, dev)
+        _need(dev_err, "dev_err", (1,), torch.int32, dev)
+        self._keep = (pool, table, length, weights, dst_table, new_length, new_weights, kept, dev_err, sh)
+        self._device = dev
+        scales = _scales(pool)
+        self._args = (ctypes.byref(sh), ctypes.byref(pool.c), scales, _ptr(table), table.shape[1], _ptr(length),
+                      _ptr(weights), stride, kept.shape[2], int(recent), _ptr(dst_table), dst_table.shape[1],
+                      _ptr(new_length), _ptr(new_weights), _ptr(kept), _ptr(dev_err))
+        self._fn = lib().kda_kv_evict
+
+    def __call__(self):
+        _launch_on(self._device, self._fn, self._args)
+
+
+def kv_evict(pool: PagePool, table, length, weights, dst_table, new_length, new_weights, kept, dev_err, **kw):
+    """Cuts every sequence longer than kept.shape[2] tokens to that many.
+
+    length: int64 [B], the cached tokens; weights: as attn_weights left them.
+    Each kv head keeps the last `recent` tokens and those of the greatest sums;
+    they go, in order, to the pages of dst_table (int32 [B][pages], pages that no
+    sequence of the call has), their sums to new_weights, and their places to
+    kept (int32 [B][Hkv][tokens to keep]).  Shorter sequences stay where they are
+    (kept -1).  new_length: int64 [B], may be length itself.  Keyword: recent.
+    """
+    KvEvictPlan(pool, table, length, weights, dst_table, new_length, new_weights, kept, dev_err, **kw)()

@@ -18,6 +18,7 @@ namespace {
 thread_local int32_t g_last_variant = KDA_VARIANT_NONE;
 
 constexpr int32_t kMaxT = 16;
+constexpr int32_t kMaxWeighed = 128;  // new tokens of a sequence in kda_attn_weights
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -143,14 +144,22 @@ kda_status check_kv_shape(const kda_kv_shape* s, const kda_pages* pages, int32_t
 
 // kda_attn_decode counts the tiles (32 tokens or more) of all sequences in 32
 // bits, and its join has a block of up to 1024 threads to each sequence.
+bool tiles_fit(const kda_kv_shape& s, int32_t page_size, int32_t max_pages) {
+  return s.B <= 1 << 20 && (int64_t)s.B * ((int64_t)max_pages * page_size / 32 + 2) <= (int64_t)1 << 30;
+}
 bool attends(const kda_kv_shape& s, int32_t page_size, int32_t max_pages) {
-  return s.T <= kMaxT && s.B <= 1 << 20 && (int64_t)s.B * ((int64_t)max_pages * page_size / 32 + 2) <= (int64_t)1 << 30;
+  return s.T <= kMaxT && tiles_fit(s, page_size, max_pages);
+}
+
+// Rows of weights have a place for every token that the table reaches.
+kda_status check_weights(const kda_pages& pages, int32_t max_pages, int64_t stride) {
+  return stride < (int64_t)max_pages * pages.page_size || stride > (int64_t)1 << 32 ? KDA_ERR_SHAPE : KDA_OK;
 }
 
 // Everything the two calls share; fills in `b` on success.
 kda_status check_kv(const kda_kv_shape* s, const kda_pages* pages, const int32_t* table, int32_t max_pages,
                     const int32_t* tok_start, int32_t n_tokens, const int64_t* pos, int32_t* dev_err,
-                    kda::KvBatch* b) {
+                    kda::KvBatch* b, bool head_scales = true) {
   kda_status r = check_kv_shape(s, pages, max_pages);
   if (r != KDA_OK) return r;
   if (n_tokens < 0 || n_tokens > 1 << 30) return KDA_ERR_SHAPE;
@@ -160,17 +169,56 @@ kda_status check_kv(const kda_kv_shape* s, const kda_pages* pages, const int32_t
     if (pages->n_pages < 1) return KDA_ERR_SHAPE;
     if (!table || !pos || !dev_err || !pages->k || (!latent && !pages->v)) return KDA_ERR_NULL;
     if (latent && pages->v) return KDA_ERR_SHAPE;
-    if (s->cache_dtype == KDA_E4M3 && (!pages->k_scale || !pages->v_scale)) return KDA_ERR_NULL;
+    const bool scaled = s->cache_dtype == KDA_E4M3 && head_scales;
+    if (scaled && (!pages->k_scale || !pages->v_scale)) return KDA_ERR_NULL;
     if (!aligned(table, 4) || !aligned(pos, 8) || !aligned(dev_err, 4) || !aligned(pages->k, 16) ||
         !aligned(pages->v, 16) || !aligned(tok_start, 4))
       return KDA_ERR_ALIGN;
-    if (s->cache_dtype == KDA_E4M3 && (!aligned(pages->k_scale, 4) || !aligned(pages->v_scale, 4)))
-      return KDA_ERR_ALIGN;
+    if (scaled && (!aligned(pages->k_scale, 4) || !aligned(pages->v_scale, 4))) return KDA_ERR_ALIGN;
   }
   int32_t shift = 0;
   while ((1 << shift) < pages->page_size) ++shift;
   *b = kda::KvBatch{*s, *pages, table, max_pages, shift, tok_start, n_tokens, pos, dev_err};
-  if (s->cache_dtype != KDA_E4M3) b->pages.k_scale = b->pages.v_scale = nullptr;
+  if (s->cache_dtype != KDA_E4M3 || !head_scales) b->pages.k_scale = b->pages.v_scale = nullptr;
+  return KDA_OK;
+}
+
+// Scales by blocks; `empty`: a call without tokens needs no pointers.
+kda_status check_scales(const kda_kv_shape& s, const kda_pages& pages, const kda_block_scales* scales, bool empty,
+                        kda::BlockScales* out) {
+  if (!scales) return KDA_ERR_NULL;
+  if (s.cache_dtype != KDA_E4M3) return KDA_ERR_DTYPE;
+  const int32_t n = scales->block;
+  if (n < 16 || n > pages.page_size || (n & (n - 1)) != 0) return KDA_ERR_SHAPE;
+  if (!empty && (!scales->k || !scales->v)) return KDA_ERR_NULL;
+  if (!aligned(scales->k, 4) || !aligned(scales->v, 4)) return KDA_ERR_ALIGN;
+  int32_t shift = 0;
+  while ((1 << shift) < n) ++shift;
+  *out = kda::BlockScales{scales->k, scales->v, shift};
+  return KDA_OK;
+}
+
+// The rotation of an append, its axes with it (null: none).
+kda_status check_rotation(const kda_kv_shape& s, const kda_rotation* rot, const kda_axes* axes, int32_t n_tokens,
+                          kda::Axes* out) {
+  *out = kda::Axes{};
+  if (axes && !rot) return KDA_ERR_NULL;
+  if (!rot) return KDA_OK;
+  if (rot->max_pos < 1 || rot->dim < 16 || rot->dim % 16 != 0 || rot->start < 0 || rot->start % 16 != 0 ||
+      (int64_t)rot->start + rot->dim > s.dk)
+    return KDA_ERR_SHAPE;
+  if (!axes) return KDA_OK;
+  if (axes->n_axes < 1 || axes->n_axes > 4 || (axes->stride != 0 && axes->stride < n_tokens) ||
+      axes->stride > (int64_t)1 << 40)
+    return KDA_ERR_SHAPE;
+  if (!axes->axis_of) return KDA_ERR_NULL;
+  out->pos = axes->pos;
+  out->stride = axes->stride ? axes->stride : n_tokens;
+  out->n = axes->n_axes;
+  for (int32_t i = 0; i < rot->dim / 2; ++i) {
+    if (axes->axis_of[i] >= axes->n_axes) return KDA_ERR_SHAPE;
+    out->of[i / 8] |= (uint16_t)(axes->axis_of[i] << 2 * (i % 8));
+  }
   return KDA_OK;
 }
 
@@ -660,55 +708,114 @@ kda_status kda_mixed_step(const kda_shape* shape, const int32_t* roles, const in
   return KDA_OK;
 }
 
+namespace {
+
+// scales null: pages with scales by heads or none.  axes null: the rotation's positions are the places.
+kda_status append_impl(const kda_kv_shape* shape, const kda_pages* pages, const kda_block_scales* scales,
+                       const int32_t* table, int32_t max_pages, const int32_t* tok_start, int32_t n_tokens,
+                       const int64_t* pos, kda::KvRows k, kda::KvRows v, kda::KvRows q, void* q_out,
+                       int64_t q_out_stride, const kda_rotation* rot, const kda_axes* axes, int32_t* dev_err,
+                       void* stream, int32_t variant) {
+  kda::KvBatch b;
+  kda_status r = check_kv(shape, pages, table, max_pages, tok_start, n_tokens, pos, dev_err, &b, !scales);
+  if (r != KDA_OK) return r;
+  const kda_kv_shape& s = *shape;
+  const bool latent = is_latent(s), empty = s.B == 0 || n_tokens == 0;
+  kda::BlockScales bs{};
+  if (scales && (r = check_scales(s, *pages, scales, empty, &bs)) != KDA_OK) return r;
+  // A thread to each unit of 16 values, and a launch has below 2^32 of them.
+  const int64_t units = ((int64_t)s.Hq * s.dk + (int64_t)s.Hkv * (s.dk + s.dv)) / 16;
+  if ((int64_t)n_tokens * units > ((int64_t)1 << 32) - 256) return KDA_ERR_SHAPE;
+  kda::Axes ax;
+  if ((r = check_rotation(s, rot, axes, n_tokens, &ax)) != KDA_OK) return r;
+  kda::KvRows qo{q_out, q_out_stride};
+  if ((r = check_rows(s, s.Hkv, s.dk, &k)) != KDA_OK || (r = check_rows(s, s.Hkv, s.dv, &v)) != KDA_OK ||
+      (r = check_rows(s, s.Hq, s.dk, &q)) != KDA_OK || (r = check_rows(s, s.Hq, s.dk, &qo)) != KDA_OK)
+    return r;
+  if (empty) return KDA_OK;
+  if (!k.p || (!latent && !v.p) || (q.p == nullptr) != (q_out == nullptr) || (q.p && !rot) ||
+      (rot && !rot->cos_sin) || (axes && !ax.pos))
+    return KDA_ERR_NULL;
+  if (latent && v.p) return KDA_ERR_SHAPE;
+  if (!aligned(k.p, 16) || !aligned(v.p, 16) || !aligned(q.p, 16) || !aligned(q_out, 16)) return KDA_ERR_ALIGN;
+  if ((rot && !aligned(rot->cos_sin, 16)) || !aligned(ax.pos, 8)) return KDA_ERR_ALIGN;
+  const kda_rotation turn = rot ? *rot : kda_rotation{};
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  return launched(scales ? kda::launch_kv_append_blocks(b, bs, k, v, q, q_out, qo.stride, turn, ax, st)
+                         : kda::launch_kv_append(b, k, v, q, q_out, qo.stride, turn, ax, st),
+                  variant);
+}
+
+kda_status attend_impl(const kda_kv_shape* shape, const kda_pages* pages, const kda_block_scales* scales,
+                       const int32_t* table, int32_t max_pages, const int32_t* tok_start, int32_t n_tokens,
+                       const int64_t* pos, kda::KvRows q, float scale, int32_t window, void* o, float* lse,
+                       void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream, int32_t variant) {
+  kda::KvBatch b;
+  kda_status r = check_kv(shape, pages, table, max_pages, tok_start, n_tokens, pos, dev_err, &b, !scales);
+  if (r != KDA_OK) return r;
+  if (!attends(*shape, pages->page_size, max_pages) || window < 0 || !isfinite(scale)) return KDA_ERR_SHAPE;
+  const bool empty = b.s.B == 0 || n_tokens == 0;
+  kda::BlockScales bs{};
+  if (scales && (r = check_scales(*shape, *pages, scales, empty, &bs)) != KDA_OK) return r;
+  if ((r = check_rows(*shape, shape->Hq, shape->dk, &q)) != KDA_OK) return r;
+  if (empty) return KDA_OK;
+  const size_t need = kda::attn_workspace_bytes(*shape, pages->page_size, max_pages);
+  if (!q.p || !o || (need > 0 && !workspace)) return KDA_ERR_NULL;
+  if (workspace_bytes < need) return KDA_ERR_SHAPE;
+  if (!aligned(q.p, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256)) return KDA_ERR_ALIGN;
+  return launched(
+      kda::launch_attn_decode(b, bs, q, scale, window, o, lse, workspace, static_cast<hipStream_t>(stream)), variant);
+}
+
+}  // namespace
+
 kda_status kda_kv_append(const kda_kv_shape* shape, const kda_pages* pages, const int32_t* table, int32_t max_pages,
                          const int32_t* tok_start, int32_t n_tokens, const int64_t* pos, const void* k,
                          int64_t k_stride, const void* v, int64_t v_stride, const void* q, int64_t q_stride,
                          void* q_out, int64_t q_out_stride, const kda_rotation* rot, int32_t* dev_err, void* stream) {
-  kda::KvBatch b;
-  kda_status r = check_kv(shape, pages, table, max_pages, tok_start, n_tokens, pos, dev_err, &b);
-  if (r != KDA_OK) return r;
-  const kda_kv_shape& s = *shape;
-  const bool latent = is_latent(s);
-  // A thread to each unit of 16 values, and a launch has below 2^32 of them.
-  const int64_t units = ((int64_t)s.Hq * s.dk + (int64_t)s.Hkv * (s.dk + s.dv)) / 16;
-  if ((int64_t)n_tokens * units > ((int64_t)1 << 32) - 256) return KDA_ERR_SHAPE;
-  if (rot) {
-    if (rot->max_pos < 1 || rot->dim < 16 || rot->dim % 16 != 0 || rot->start < 0 || rot->start % 16 != 0 ||
-        (int64_t)rot->start + rot->dim > s.dk)
-      return KDA_ERR_SHAPE;
-  }
-  kda::KvRows kr{k, k_stride}, vr{v, v_stride}, qr{q, q_stride}, qo{q_out, q_out_stride};
-  if ((r = check_rows(s, s.Hkv, s.dk, &kr)) != KDA_OK || (r = check_rows(s, s.Hkv, s.dv, &vr)) != KDA_OK ||
-      (r = check_rows(s, s.Hq, s.dk, &qr)) != KDA_OK || (r = check_rows(s, s.Hq, s.dk, &qo)) != KDA_OK)
-    return r;
-  if (b.s.B == 0 || n_tokens == 0) return KDA_OK;
-  if (!k || (!latent && !v) || (q == nullptr) != (q_out == nullptr) || (q && !rot) || (rot && !rot->cos_sin))
-    return KDA_ERR_NULL;
-  if (latent && v) return KDA_ERR_SHAPE;
-  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16)) return KDA_ERR_ALIGN;
-  if (rot && !aligned(rot->cos_sin, 16)) return KDA_ERR_ALIGN;
-  return launched(kda::launch_kv_append(b, kr, vr, qr, q_out, qo.stride, rot ? *rot : kda_rotation{},
-                                        static_cast<hipStream_t>(stream)),
-                  KDA_VARIANT_KV_APPEND);
+  return append_impl(shape, pages, nullptr, table, max_pages, tok_start, n_tokens, pos, kda::KvRows{k, k_stride},
+                     kda::KvRows{v, v_stride}, kda::KvRows{q, q_stride}, q_out, q_out_stride, rot, nullptr, dev_err,
+                     stream, KDA_VARIANT_KV_APPEND);
+}
+
+kda_status kda_kv_append_axes(const kda_kv_shape* shape, const kda_pages* pages, const int32_t* table,
+                              int32_t max_pages, const int32_t* tok_start, int32_t n_tokens, const int64_t* pos,
+                              const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+                              int64_t q_stride, void* q_out, int64_t q_out_stride, const kda_rotation* rot,
+                              const kda_axes* axes, int32_t* dev_err, void* stream) {
+  if (!axes) return KDA_ERR_NULL;
+  return append_impl(shape, pages, nullptr, table, max_pages, tok_start, n_tokens, pos, kda::KvRows{k, k_stride},
+                     kda::KvRows{v, v_stride}, kda::KvRows{q, q_stride}, q_out, q_out_stride, rot, axes, dev_err,
+                     stream, KDA_VARIANT_KV_APPEND_AXES);
+}
+
+kda_status kda_kv_append_blocks(const kda_kv_shape* shape, const kda_pages* pages, const kda_block_scales* scales,
+                                const int32_t* table, int32_t max_pages, const int32_t* tok_start, int32_t n_tokens,
+                                const int64_t* pos, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                                const kda_rotation* rot, const kda_axes* axes, int32_t* dev_err, void* stream) {
+  if (!scales) return KDA_ERR_NULL;
+  return append_impl(shape, pages, scales, table, max_pages, tok_start, n_tokens, pos, kda::KvRows{k, k_stride},
+                     kda::KvRows{v, v_stride}, kda::KvRows{q, q_stride}, q_out, q_out_stride, rot, axes, dev_err,
+                     stream, KDA_VARIANT_KV_APPEND_BLOCKS);
 }
 
 kda_status kda_attn_decode(const kda_kv_shape* shape, const kda_pages* pages, const int32_t* table,
                            int32_t max_pages, const int32_t* tok_start, int32_t n_tokens, const int64_t* pos,
                            const void* q, int64_t q_stride, float scale, int32_t window, void* o, float* lse,
                            void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream) {
-  kda::KvBatch b;
-  kda_status r = check_kv(shape, pages, table, max_pages, tok_start, n_tokens, pos, dev_err, &b);
-  if (r != KDA_OK) return r;
-  if (!attends(*shape, pages->page_size, max_pages) || window < 0 || !isfinite(scale)) return KDA_ERR_SHAPE;
-  kda::KvRows qr{q, q_stride};
-  if ((r = check_rows(*shape, shape->Hq, shape->dk, &qr)) != KDA_OK) return r;
-  if (b.s.B == 0 || n_tokens == 0) return KDA_OK;
-  const size_t need = kda::attn_workspace_bytes(*shape, pages->page_size, max_pages);
-  if (!q || !o || (need > 0 && !workspace)) return KDA_ERR_NULL;
-  if (workspace_bytes < need) return KDA_ERR_SHAPE;
-  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256)) return KDA_ERR_ALIGN;
-  return launched(kda::launch_attn_decode(b, qr, scale, window, o, lse, workspace, static_cast<hipStream_t>(stream)),
-                  KDA_VARIANT_ATTN_DECODE);
+  return attend_impl(shape, pages, nullptr, table, max_pages, tok_start, n_tokens, pos, kda::KvRows{q, q_stride}, scale,
+                     window, o, lse, workspace, workspace_bytes, dev_err, stream, KDA_VARIANT_ATTN_DECODE);
+}
+
+kda_status kda_attn_decode_blocks(const kda_kv_shape* shape, const kda_pages* pages, const kda_block_scales* scales,
+                                  const int32_t* table, int32_t max_pages, const int32_t* tok_start, int32_t n_tokens,
+                                  const int64_t* pos, const void* q, int64_t q_stride, float scale, int32_t window,
+                                  void* o, float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                  void* stream) {
+  if (!scales) return KDA_ERR_NULL;
+  return attend_impl(shape, pages, scales, table, max_pages, tok_start, n_tokens, pos, kda::KvRows{q, q_stride}, scale,
+                     window, o, lse, workspace, workspace_bytes, dev_err, stream, KDA_VARIANT_ATTN_DECODE_BLOCKS);
 }
 
 size_t kda_attn_workspace_bytes(const kda_kv_shape* shape, const kda_pages* pages, int32_t max_pages) {
@@ -720,6 +827,59 @@ size_t kda_attn_workspace_bytes(const kda_kv_shape* shape, const kda_pages* page
     if (n > most) most = n;
   }
   return most;
+}
+
+kda_status kda_attn_weights(const kda_kv_shape* shape, const kda_pages* pages, const kda_block_scales* scales,
+                            const int32_t* table, int32_t max_pages, const int32_t* tok_start, int32_t n_tokens,
+                            const int64_t* pos, const void* q, int64_t q_stride, float scale, int32_t window,
+                            const float* lse, float* weights, int64_t weights_stride, int32_t* dev_err, void* stream) {
+  kda::KvBatch b;
+  kda_status r = check_kv(shape, pages, table, max_pages, tok_start, n_tokens, pos, dev_err, &b, !scales);
+  if (r != KDA_OK) return r;
+  const kda_kv_shape& s = *shape;
+  if (is_latent(s) || s.T > kMaxWeighed || !tiles_fit(s, pages->page_size, max_pages)) return KDA_ERR_SHAPE;
+  if (window < 0 || !isfinite(scale)) return KDA_ERR_SHAPE;
+  const bool empty = s.B == 0 || n_tokens == 0;
+  kda::BlockScales bs{};
+  if (scales && (r = check_scales(s, *pages, scales, empty, &bs)) != KDA_OK) return r;
+  if ((r = check_weights(*pages, max_pages, weights_stride)) != KDA_OK) return r;
+  kda::KvRows qr{q, q_stride};
+  if ((r = check_rows(s, s.Hq, s.dk, &qr)) != KDA_OK) return r;
+  if (empty) return KDA_OK;
+  if (!q || !lse || !weights) return KDA_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(lse, 4) || !aligned(weights, 4)) return KDA_ERR_ALIGN;
+  return launched(kda::launch_attn_weights(b, bs, qr, scale, window, lse, weights, weights_stride,
+                                           static_cast<hipStream_t>(stream)),
+                  KDA_VARIANT_ATTN_WEIGHTS);
+}
+
+kda_status kda_kv_evict(const kda_kv_shape* shape, const kda_pages* pages, const kda_block_scales* scales,
+                        const int32_t* table, int32_t max_pages, const int64_t* len, const float* weights,
+                        int64_t weights_stride, int32_t keep, int32_t recent, const int32_t* dst_table,
+                        int32_t dst_max_pages, int64_t* new_len, float* new_weights, int32_t* kept, int32_t* dev_err,
+                        void* stream) {
+  kda::KvBatch b;
+  kda_kv_shape s = shape ? *shape : kda_kv_shape{};
+  s.T = 1;  // the call brings no tokens: the checks ask for one of each sequence
+  kda_status r = shape ? check_kv_shape(shape, pages, max_pages) : KDA_ERR_NULL;
+  if (r != KDA_OK) return r;
+  if ((r = check_kv(&s, pages, table, max_pages, nullptr, s.B, len, dev_err, &b, !scales)) != KDA_OK) return r;
+  // Workgroups of up to 1024 threads to each (sequence, kv head), of keys and of values.
+  if ((int64_t)s.B * s.Hkv > (int64_t)1 << 20) return KDA_ERR_SHAPE;
+  const bool empty = s.B == 0;
+  kda::BlockScales bs{};
+  if (scales && (r = check_scales(s, *pages, scales, empty, &bs)) != KDA_OK) return r;
+  if ((r = check_weights(*pages, max_pages, weights_stride)) != KDA_OK) return r;
+  if (dst_max_pages < 1 || (int64_t)dst_max_pages * pages->page_size > (int64_t)1 << 30) return KDA_ERR_SHAPE;
+  if (keep < 1 || keep > dst_max_pages * pages->page_size || recent < 0 || recent > keep) return KDA_ERR_SHAPE;
+  if (empty) return KDA_OK;
+  if (!weights || !dst_table || !new_len || !new_weights || !kept) return KDA_ERR_NULL;
+  if (!aligned(weights, 4) || !aligned(dst_table, 4) || !aligned(new_len, 8) || !aligned(new_weights, 4) ||
+      !aligned(kept, 4))
+    return KDA_ERR_ALIGN;
+  return launched(kda::launch_kv_evict(b, bs, weights, weights_stride, keep, recent, dst_table, dst_max_pages, new_len,
+                                       new_weights, kept, static_cast<hipStream_t>(stream)),
+                  KDA_VARIANT_KV_EVICT);
 }
 
 const char* kda_status_str(kda_status status) {

@@ -39,280 +39,12 @@
 
 #include <type_traits>
 
-#include "kda_attn_impl.h"
+#include "kda_attn_cache.h"
 
 namespace kda {
 namespace {
 
 constexpr int kWaves = 4;
-
-typedef __attribute__((ext_vector_type(2))) uint16_t u16x2;
-
-__device__ __forceinline__ float widen(bf16_t x) { return __uint_as_float((uint32_t)x << 16); }
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ float widen(uint8_t x) { return __builtin_amdgcn_cvt_f32_fp8((int)x, 0); }
-// Two e4m3 values (the low or high pair of w) as packed bf16, exactly.
-template <bool HI>
-__device__ __forceinline__ uint32_t widen_e4m3(uint32_t w) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, HI));
-}
-
-// The probabilities of 32 tokens as an operand, and products with V^T tiles:
-// w holds two neighbouring columns of the lane's eight tokens.
-template <int NQ>
-struct Weights {
-  bf16x8 p[NQ];
-
-  __device__ __forceinline__ explicit Weights(const f32x4 (&x)[NQ][2]) {
-#pragma unroll
-    for (int n = 0; n < NQ; ++n)
-      p[n] = as_op(pack2(x[n][0][0], x[n][0][1]), pack2(x[n][0][2], x[n][0][3]), pack2(x[n][1][0], x[n][1][1]),
-                   pack2(x[n][1][2], x[n][1][3]));
-  }
-  template <int VC>
-  __device__ __forceinline__ void add(const uint32_t (&w)[8], bool high, f32x4 (&out)[NQ][VC], int c) const {
-    uint32_t x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      x[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], high ? 0x07060302u : 0x05040100u);
-    const bf16x8 vt = as_op(x[0], x[1], x[2], x[3]);
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) out[n][c] = mfma_bf16(vt, p[n], out[n][c]);
-  }
-};
-
-template <bool NT, typename V, typename T>
-__device__ __forceinline__ V load(const T* p) {
-  const V* v = reinterpret_cast<const V*>(p);
-  return NT ? __builtin_nontemporal_load(v) : *v;
-}
-
-// One wave's share of the keys and values of SUB tokens, in the layout that
-// the loads give, and the operands made from it.  Token t of the share is row
-// `t & 15` of group `t >> 4`; pk / pv point to each group's first row.
-//
-// NT: loads that leave the caches to others (see run()).
-//
-// bf16: 32 tokens, 32 contraction slots.
-template <int D, typename TC, bool NT>
-struct Cache;
-
-template <int D, bool NT>
-struct Cache<D, bf16_t, NT> {
-  static constexpr int GROUPS = 2, SUB = 32;
-  static constexpr int VC = D / 16;  // neighbouring values of a row in a lane
-  u32x4 k[2][D / 32];
-  uint32_t v[8][VC / 2];
-  struct Query {
-    bf16x8 q[D / 32];
-  };
-
-  static __device__ __forceinline__ void load_query(Query& q, const bf16_t* row, bool live) {
-    const int g = (threadIdx.x & 63) >> 4;
-#pragma unroll
-    for (int s = 0; s < D / 32; ++s)
-      q.q[s] = live ? *reinterpret_cast<const bf16x8*>(row + 32 * s + 8 * g) : bf16x8{};
-  }
-  __device__ __forceinline__ void load_k(int u, const bf16_t* rows) {
-    const int l = threadIdx.x & 63;
-#pragma unroll
-    for (int s = 0; s < D / 32; ++s)
-      k[u][s] = load<NT, u32x4>(rows + (l & 15) * D + 32 * s + 8 * (l >> 4));
-  }
-  __device__ __forceinline__ void load_v(int u, const bf16_t* rows) {
-    const int l = threadIdx.x & 63;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bf16_t* p = rows + (4 * (l >> 4) + j) * D + VC * (l & 15);
-      if constexpr (VC == 8) {
-        const u32x4 w = load<NT, u32x4>(p);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[4 * u + j][i] = w[i];
-      } else {
-        const u32x2 w = load<NT, u32x2>(p);
-        v[4 * u + j][0] = w[0];
-        v[4 * u + j][1] = w[1];
-      }
-    }
-  }
-  __device__ __forceinline__ f32x4 score(int u, const Query& q) const {
-    f32x4 c = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int s = 0; s < D / 32; ++s) c = mfma_bf16(__builtin_bit_cast(bf16x8, k[u][s]), q.q[s], c);
-    return c;
-  }
-  // Values of the lane's token e (of 8: group e >> 2): zero unless kept / tested.
-  __device__ __forceinline__ void keep(int e, bool kept) {
-#pragma unroll
-    for (int i = 0; i < VC / 2; ++i) v[e][i] = kept ? v[e][i] : 0;
-  }
-  // What of `acc` and token e tells a value that is not finite: the largest
-  // magnitude of the low and of the high halves.
-  __device__ __forceinline__ uint32_t peak(int e, uint32_t acc) const {
-#pragma unroll
-    for (int i = 0; i < VC / 2; ++i)
-      acc = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, acc),
-                                                                   __builtin_bit_cast(u16x2, v[e][i] & 0x7fff7fffu)));
-    return acc;
-  }
-  static __device__ __forceinline__ bool not_finite(uint32_t acc) {
-    return (acc & 0xffffu) >= 0x7f80u || acc >= 0x7f800000u;
-  }
-  // out[c] += V^T tile c times the probabilities.
-  template <int NQ>
-  __device__ __forceinline__ void weigh(const f32x4 (&p)[NQ][2], f32x4 (&out)[NQ][VC]) const {
-    const Weights<NQ> weights(p);
-#pragma unroll
-    for (int c = 0; c < VC; ++c) {
-      uint32_t w[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = v[e][c / 2];
-      weights.add(w, c & 1, out, c);
-    }
-  }
-};
-
-// e4m3: as bf16, widened when used.  A key load of 16 bytes feeds two
-// contraction steps, so the queries are laid out to match.
-template <int D, bool NT>
-struct Cache<D, uint8_t, NT> {
-  static constexpr int GROUPS = 2, SUB = 32;
-  static constexpr int VC = D / 16;
-  u32x4 k[2][D / 64];
-  uint32_t v[8][VC / 4];
-  struct Query {
-    bf16x8 q[D / 32];
-  };
-
-  static __device__ __forceinline__ void load_query(Query& q, const bf16_t* row, bool live) {
-    const int g = (threadIdx.x & 63) >> 4;
-#pragma unroll
-    for (int s = 0; s < D / 32; ++s)
-      q.q[s] = live ? *reinterpret_cast<const bf16x8*>(row + 64 * (s / 2) + 16 * g + 8 * (s & 1)) : bf16x8{};
-  }
-  __device__ __forceinline__ void load_k(int u, const uint8_t* rows) {
-    const int l = threadIdx.x & 63;
-#pragma unroll
-    for (int s = 0; s < D / 64; ++s)
-      k[u][s] = load<NT, u32x4>(rows + (l & 15) * D + 64 * s + 16 * (l >> 4));
-  }
-  __device__ __forceinline__ void load_v(int u, const uint8_t* rows) {
-    const int l = threadIdx.x & 63;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint8_t* p = rows + (4 * (l >> 4) + j) * D + VC * (l & 15);
-      if constexpr (VC == 8) {
-        const u32x2 w = load<NT, u32x2>(p);
-        v[4 * u + j][0] = w[0];
-        v[4 * u + j][1] = w[1];
-      } else {
-        v[4 * u + j][0] = load<NT, uint32_t>(p);
-      }
-    }
-  }
-  __device__ __forceinline__ f32x4 score(int u, const Query& q) const {
-    f32x4 c = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int s = 0; s < D / 32; ++s) {
-      const uint32_t a = k[u][s / 2][2 * (s & 1)], b = k[u][s / 2][2 * (s & 1) + 1];
-      c = mfma_bf16(as_op(widen_e4m3<false>(a), widen_e4m3<true>(a), widen_e4m3<false>(b), widen_e4m3<true>(b)),
-                    q.q[s], c);
-    }
-    return c;
-  }
-  __device__ __forceinline__ void keep(int e, bool kept) {
-#pragma unroll
-    for (int i = 0; i < VC / 4; ++i) v[e][i] = kept ? v[e][i] : 0;
-  }
-  // The type has NaN only, all ones but the sign: adding one carries into it.
-  __device__ __forceinline__ uint32_t peak(int e, uint32_t acc) const {
-#pragma unroll
-    for (int i = 0; i < VC / 4; ++i) acc |= (v[e][i] & 0x7f7f7f7fu) + 0x01010101u;
-    return acc;
-  }
-  static __device__ __forceinline__ bool not_finite(uint32_t acc) { return (acc & 0x80808080u) != 0; }
-  template <int NQ>
-  __device__ __forceinline__ void weigh(const f32x4 (&p)[NQ][2], f32x4 (&out)[NQ][VC]) const {
-    const Weights<NQ> weights(p);
-#pragma unroll
-    for (int c = 0; c < VC; c += 2) {
-      uint32_t w[8];  // columns c and c + 1 of the lane's tokens
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = c & 2 ? widen_e4m3<true>(v[e][c / 4]) : widen_e4m3<false>(v[e][c / 4]);
-      weights.add(w, false, out, c);
-      weights.add(w, true, out, c + 1);
-    }
-  }
-};
-
-// fp32: 16 tokens; a contraction step takes four k-slots, one to each lane
-// group.  V^T tile (64 h + c): columns 64 h + 4 m + c.
-template <int D, bool NT>
-struct Cache<D, float, NT> {
-  static constexpr int GROUPS = 1, SUB = 16;
-  static constexpr int VC = D / 16;
-  f32x4 k[1][D / 16];
-  f32x4 v[4][D / 64];
-  struct Query {
-    f32x4 q[D / 16];
-  };
-
-  static __device__ __forceinline__ void load_query(Query& q, const float* row, bool live) {
-    const int g = (threadIdx.x & 63) >> 4;
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-      q.q[s] = live ? *reinterpret_cast<const f32x4*>(row + 16 * s + 4 * g) : f32x4{};
-  }
-  __device__ __forceinline__ void load_k(int u, const float* rows) {
-    const int l = threadIdx.x & 63;
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-      k[u][s] = load<NT, f32x4>(rows + (l & 15) * D + 16 * s + 4 * (l >> 4));
-  }
-  __device__ __forceinline__ void load_v(int, const float* rows) {
-    const int l = threadIdx.x & 63;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h)
-        v[j][h] = load<NT, f32x4>(rows + (4 * (l >> 4) + j) * D + 64 * h + 4 * (l & 15));
-  }
-  __device__ __forceinline__ f32x4 score(int u, const Query& q) const {
-    f32x4 c = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(k[u][s][i], q.q[s][i], c, 0, 0, 0);
-    return c;
-  }
-  __device__ __forceinline__ void keep(int e, bool kept) {
-#pragma unroll
-    for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[e][h][i] = kept ? v[e][h][i] : 0.f;
-  }
-  __device__ __forceinline__ uint32_t peak(int e, uint32_t acc) const {
-#pragma unroll
-    for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc = max(acc, __float_as_uint(v[e][h][i]) & 0x7fffffffu);
-    return acc;
-  }
-  static __device__ __forceinline__ bool not_finite(uint32_t acc) { return acc >= 0x7f800000u; }
-  template <int NQ>
-  __device__ __forceinline__ void weigh(const f32x4 (&p)[NQ][1], f32x4 (&out)[NQ][VC]) const {
-#pragma unroll
-    for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int n = 0; n < NQ; ++n)
-            out[n][4 * h + c] =
-                __builtin_amdgcn_mfma_f32_16x16x4f32(v[j][h][c], p[n][0][j], out[n][4 * h + c], 0, 0, 0);
-  }
-};
 
 // Column of the output that register i of tile c holds in lane group g.
 template <int D, typename TC>
@@ -321,8 +53,8 @@ __device__ __forceinline__ int out_col(int g, int c, int i) {
   return D / 16 * (4 * g + i) + c;
 }
 
-// NQ blocks of 16 query rows to a workgroup.
-template <int D, typename TIn, typename TC, int NQ, bool NT>
+// NQ blocks of 16 query rows to a workgroup.  BLK: scales by blocks of tokens.
+template <int D, typename TIn, typename TC, int NQ, bool NT, bool BLK>
 __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1) attn_kernel(AttnArgs a) {
   typedef Cache<D, TC, NT> C;
   constexpr int SUB = C::SUB, GROUPS = C::GROUPS, VC = C::VC, TILE = kWaves * SUB;
@@ -336,8 +68,8 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
   const int G = kb.s.Hq / kb.s.Hkv;
   Run<TILE> run(a, worker, worker == 0 && hk == 0 && rb == 0 && wave == 0);
   float x_scale = a.scale * kLog2e;
-  if (sizeof(TC) == 1) x_scale *= kb.pages.k_scale[hk];
-  const float v_scale = sizeof(TC) == 1 ? kb.pages.v_scale[hk] : 1.f;
+  if (sizeof(TC) == 1 && !BLK) x_scale *= kb.pages.k_scale[hk];
+  const float v_scale = sizeof(TC) == 1 && !BLK ? kb.pages.v_scale[hk] : 1.f;
 
   while (run.tile < run.end) {
     const Seq& s = run.s;
@@ -377,24 +109,46 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
       const TC* const pages_v = static_cast<const TC*>(kb.pages.v);
       int32_t id[GROUPS];  // page entries of the tile to be loaded next
       int64_t at[GROUPS];
+      // Scales of the groups' blocks (a group lies in one, and it or the one that
+      // stands for it has visible tokens), of keys and values that are on their
+      // way; of those being scored, times x_scale.
+      float k_block[GROUPS], v_block[GROUPS], x_block[GROUPS];
       auto load_k = [&](int token) {
 #pragma unroll
         for (int u = 0; u < GROUPS; ++u) {
           at[u] = walk.row(token + 16 * u, id[u]);
           cache.load_k(u, pages_k + at[u] * D);
+          if constexpr (BLK) k_block[u] = block_scale(a.scales.k, a.scales.shift, at[u]);
           id[u] = walk.entry(token + TILE + 16 * u);
         }
       };
       auto load_v = [&] {
 #pragma unroll
-        for (int u = 0; u < GROUPS; ++u) cache.load_v(u, pages_v + at[u] * D);
+        for (int u = 0; u < GROUPS; ++u) {
+          cache.load_v(u, pages_v + at[u] * D);
+          if constexpr (BLK) v_block[u] = block_scale(a.scales.v, a.scales.shift, at[u]);
+        }
       };
       f32x4 p[NQ][GROUPS];
       auto scores = [&] {
 #pragma unroll
-        for (int u = 0; u < GROUPS; ++u)
+        for (int u = 0; u < GROUPS; ++u) {
+          x_block[u] = BLK ? x_scale * k_block[u] : x_scale;
 #pragma unroll
           for (int n = 0; n < NQ; ++n) p[n][u] = cache.score(u, q[n]);
+        }
+      };
+      // O^T += V^T P^T, with blocks' scales in the probabilities (powers of two
+      // there lose nothing).
+      auto weigh = [&] {
+        if constexpr (BLK)
+#pragma unroll
+          for (int u = 0; u < GROUPS; ++u)
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) p[n][u][i] *= v_block[u];
+        cache.weigh(p, out);
       };
       // Scores to probabilities, and the earlier sums to the new maximum.
       // PART: some row does not see some token.
@@ -409,7 +163,7 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
           for (int u = 0; u < GROUPS; ++u)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float x = p[n][u][i] * x_scale;
+              float x = p[n][u][i] * x_block[u];
               const int j = t0 + 16 * u + 4 * g + i;
               if (PART && (j > vis[n] || j <= low)) x = -INFINITY;
               p[n][u][i] = x;
@@ -446,7 +200,7 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
           scores();
           load_k(t0 + TILE);
           softmax(std::false_type{});
-          cache.weigh(p, out);
+          weigh();
           load_v();
         }
         scores();
@@ -482,9 +236,11 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             for (int j = max(t0, s.lo); j < min(t0 + SUB, s.end); ++j) {
               if (j >= all_lo && j <= s.pos) continue;
-              const float w = plane[(j - t0) * 16 + col];
+              float w = plane[(j - t0) * 16 + col];
               const bool sees = j <= vis[n] && (a.window == 0 || j > vis[n] - a.window);
-              const TC* const v = pages_v + (walk.row(j & ~15, walk.entry(j)) + (j & 15)) * D;
+              const int64_t group = walk.row(j & ~15, walk.entry(j));
+              if constexpr (BLK) w *= block_scale(a.scales.v, a.scales.shift, group);
+              const TC* const v = pages_v + (group + (j & 15)) * D;
 #pragma unroll
               for (int c = 0; c < VC; ++c)
 #pragma unroll
@@ -495,7 +251,7 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
             }
           }
         }
-        cache.weigh(p, out);
+        weigh();
         t0 += TILE;
       }
 
@@ -580,25 +336,25 @@ Split split_of(const kda_kv_shape& s, int32_t page_size, int32_t max_pages) {
 // 88 at 64 of up to 8191, 116 -> 107 in e4m3.  A smaller one may still be there
 // from the call before, and is then read from there: 25 us with plain loads
 // against 29 for 16 sequences whose three pools of 78 MB took turns.
-template <int D, typename TIn, typename TC, int NQ>
+template <int D, typename TIn, typename TC, int NQ, bool BLK>
 hipError_t run(const AttnArgs& a, hipStream_t st) {
   const dim3 grid(a.workers, a.kb.s.Hkv, a.row_blocks), block(kWaves * kWave);
   if (outgrows_cache(a.kb))
-    hipLaunchKernelGGL((attn_kernel<D, TIn, TC, NQ, true>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((attn_kernel<D, TIn, TC, NQ, true, BLK>), grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL((attn_kernel<D, TIn, TC, NQ, false>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((attn_kernel<D, TIn, TC, NQ, false, BLK>), grid, block, 0, st, a);
   const hipError_t e = hipGetLastError();
   return e != hipSuccess ? e : run_join<D, TIn>(a, st);
 }
 
-template <typename TIn, typename TC>
+template <typename TIn, typename TC, bool BLK = false>
 hipError_t by_size(const AttnArgs& a, hipStream_t st) {
   const bool wide = a.kb.s.dk == 128;
   switch (a.rows) {
-    case 16: return wide ? run<128, TIn, TC, 1>(a, st) : run<64, TIn, TC, 1>(a, st);
-    case 32: return wide ? run<128, TIn, TC, 2>(a, st) : run<64, TIn, TC, 2>(a, st);
+    case 16: return wide ? run<128, TIn, TC, 1, BLK>(a, st) : run<64, TIn, TC, 1, BLK>(a, st);
+    case 32: return wide ? run<128, TIn, TC, 2, BLK>(a, st) : run<64, TIn, TC, 2, BLK>(a, st);
   }
-  if constexpr (sizeof(TIn) == 2) return wide ? run<128, TIn, TC, 4>(a, st) : run<64, TIn, TC, 4>(a, st);
+  if constexpr (sizeof(TIn) == 2) return wide ? run<128, TIn, TC, 4, BLK>(a, st) : run<64, TIn, TC, 4, BLK>(a, st);
   return hipErrorInvalidValue;
 }
 
@@ -609,12 +365,13 @@ size_t attn_workspace_bytes(const kda_kv_shape& s, int32_t page_size, int32_t ma
   return workspace_of(s, split_of(s, page_size, max_pages)).total;
 }
 
-hipError_t launch_attn_decode(const KvBatch& b, KvRows q, float scale, int32_t window, void* o, float* lse,
-                              void* workspace, hipStream_t st) {
+hipError_t launch_attn_decode(const KvBatch& b, const BlockScales& scales, KvRows q, float scale, int32_t window,
+                              void* o, float* lse, void* workspace, hipStream_t st) {
   if (b.s.dk == 576) return launch_attn_latent(b, q, scale, window, o, lse, workspace, st);
   const AttnArgs a =
-      make_args(b, q, scale, window, o, lse, workspace, split_of(b.s, b.pages.page_size, b.max_pages));
+      make_args(b, scales, q, scale, window, o, lse, workspace, split_of(b.s, b.pages.page_size, b.max_pages));
   if (b.s.in_dtype == KDA_F32) return by_size<float, float>(a, st);
+  if (scales.k) return by_size<bf16_t, uint8_t, true>(a, st);
   if (b.s.cache_dtype == KDA_E4M3) return by_size<bf16_t, uint8_t>(a, st);
   return by_size<bf16_t, bf16_t>(a, st);
 }

@@ -36,6 +36,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 
 struct AttnArgs {
   KvBatch kb;
+  BlockScales scales;
   KvRows q;
   float scale;
   int32_t window;
@@ -50,7 +51,7 @@ struct AttnArgs {
   // Workspace: each sequence's first and last worker [B], then for every piece
   // (worker, slot, kv head, row block) its rows' (max, sum) and outputs.  A sum
   // below zero refuses the sequence.
-  int2* span;
+  int2* span;  // null: no pieces are joined
   f32x2* piece_ml;
   float* piece_o;
 };
@@ -117,19 +118,6 @@ __device__ __forceinline__ Seq seq_of_lane(const Seq& x, int from) {
   s.tiles = __builtin_amdgcn_readlane(x.tiles, from);
   s.err = 0;
   return s;
-}
-
-// Inclusive sum over the wave's lanes: inside each 16-lane row by shifts of 1,
-// 2, 4 and 8, then the last lane of a row to the row after it and of the lower
-// half to the upper.  No LDS, no barrier.
-__device__ __forceinline__ int32_t wave_scan(int32_t x) {
-  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);   // row_shr:1
-  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);   // row_shr:2
-  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);   // row_shr:4
-  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);   // row_shr:8
-  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1 and 3
-  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2 and 3
-  return x;
 }
 
 // How `total` places of the list fall to the workers: `count` of them have a run (none is
@@ -227,7 +215,7 @@ struct Run {
       upto = wave_scan(count);
       if (__builtin_amdgcn_readlane(upto, kWave - 1) <= a.workers) break;
     }
-    if (record && lane < a.kb.s.B) a.span[lane] = make_int2(upto - count, max(upto - 1, upto - count));
+    if (record && a.span && lane < a.kb.s.B) a.span[lane] = make_int2(upto - count, max(upto - 1, upto - count));
     const uint64_t past = __ballot(upto > worker);
     if (past == 0) return;
     b = __ffsll((unsigned long long)past) - 1;
@@ -243,7 +231,7 @@ struct Run {
 
   // Sequence `seq`, whose tiles end before place `upto`.
   __device__ __forceinline__ void write_span(const Shares& shares, int seq, int32_t upto, int32_t tiles) const {
-    if (seq < a.kb.s.B)
+    if (a.span && seq < a.kb.s.B)
       a.span[seq] = tiles > 0 ? make_int2(shares.of(upto - tiles), shares.of(upto - 1)) : make_int2(0, 0);
   }
 
@@ -462,11 +450,11 @@ inline Workspace workspace_of(const kda_kv_shape& s, const Split& d) {
   return L;
 }
 
-inline AttnArgs make_args(const KvBatch& b, KvRows q, float scale, int32_t window, void* o, float* lse,
+inline AttnArgs make_args(const KvBatch& b, const BlockScales& scales, KvRows q, float scale, int32_t window, void* o, float* lse,
                           void* workspace, const Split& d) {
   const Workspace L = workspace_of(b.s, d);
   char* ws = static_cast<char*>(workspace);
-  return AttnArgs{b,         q,
+  return AttnArgs{b, scales, q,
                   scale,     window,
                   o,         lse,
                   d.workers, d.run_tiles, d.start_tiles, d.few, d.row_blocks,

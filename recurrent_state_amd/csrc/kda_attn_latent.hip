@@ -447,7 +447,7 @@ size_t latent_workspace_bytes(const kda_kv_shape& s, int32_t page_size, int32_t 
 hipError_t launch_attn_latent(const KvBatch& b, KvRows q, float scale, int32_t window, void* o, float* lse,
                               void* workspace, hipStream_t st) {
   const Split d = split_of(b.s, b.pages.page_size, b.max_pages);
-  const AttnArgs a = make_args(b, q, scale, window, o, lse, workspace, d);
+  const AttnArgs a = make_args(b, BlockScales{}, q, scale, window, o, lse, workspace, d);
   return d.rows == 16   ? run<1>(a, st)
          : d.rows == 32 ? run<2>(a, st)
          : d.rows == 64 ? run<4>(a, st)

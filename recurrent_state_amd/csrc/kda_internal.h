@@ -129,16 +129,39 @@ struct KvRows {  // token rows `stride` elements apart
   const void* p;
   int64_t stride;
 };
+// Positions of rotations on several axes; n = 0: the places in the cache.
+struct Axes {
+  const int64_t* pos;  // [n] rows `stride` apart
+  int64_t stride;
+  int32_t n;
+  uint16_t of[36];  // the axes of 8 pairs, two bits each
+};
+// Scales of e4m3 pages by blocks; k null: the pool's own.
+struct BlockScales {
+  float* k;
+  float* v;
+  int32_t shift;  // log2(block)
+};
 // rot.cos_sin null: keys are stored as they are.  q.p null: no queries.
 hipError_t launch_kv_append(const KvBatch& b, KvRows k, KvRows v, KvRows q, void* q_out, int64_t q_out_stride,
-                            const kda_rotation& rot, hipStream_t st);
-hipError_t launch_attn_decode(const KvBatch& b, KvRows q, float scale, int32_t window, void* o, float* lse,
-                              void* workspace, hipStream_t st);
+                            const kda_rotation& rot, const Axes& axes, hipStream_t st);
+hipError_t launch_kv_append_blocks(const KvBatch& b, const BlockScales& scales, KvRows k, KvRows v, KvRows q,
+                                   void* q_out, int64_t q_out_stride, const kda_rotation& rot, const Axes& axes,
+                                   hipStream_t st);
+hipError_t launch_attn_decode(const KvBatch& b, const BlockScales& scales, KvRows q, float scale, int32_t window,
+                              void* o, float* lse, void* workspace, hipStream_t st);
 size_t attn_workspace_bytes(const kda_kv_shape& s, int32_t page_size, int32_t max_pages);
 // Their latent form.
 hipError_t launch_attn_latent(const KvBatch& b, KvRows q, float scale, int32_t window, void* o, float* lse,
                               void* workspace, hipStream_t st);
 size_t latent_workspace_bytes(const kda_kv_shape& s, int32_t page_size, int32_t max_pages);
+
+hipError_t launch_attn_weights(const KvBatch& b, const BlockScales& scales, KvRows q, float scale, int32_t window,
+                               const float* lse, float* weights, int64_t stride, hipStream_t st);
+// b.pos: the lengths.
+hipError_t launch_kv_evict(const KvBatch& b, const BlockScales& scales, const float* weights, int64_t stride,
+                           int32_t keep, int32_t recent, const int32_t* dst_table, int32_t dst_max_pages,
+                           int64_t* new_len, float* new_weights, int32_t* kept, hipStream_t st);
 
 // Copies whole per-sequence states (n_floats each) and positions for up to
 // kMaxPairs (src, dst) index pairs per launch.

@@ -19,6 +19,19 @@ __device__ __forceinline__ int here(int x) {
   return x;
 }
 
+// Inclusive sum over the wave's lanes: inside each 16-lane row by shifts of 1,
+// 2, 4 and 8, then the last lane of a row to the row after it and of the lower
+// half to the upper.  No LDS, no barrier.
+__device__ __forceinline__ int32_t wave_scan(int32_t x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);   // row_shr:1
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);   // row_shr:2
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);   // row_shr:4
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);   // row_shr:8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2 and 3
+  return x;
+}
+
 // The new tokens of sequence b: packed rows row0 .. row0 + n - 1.  n = 0 for a
 // sequence that sits the call out; bad: its range does not fit the launch.
 struct SeqRows {

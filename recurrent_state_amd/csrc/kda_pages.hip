@@ -17,7 +17,7 @@
 // (2.50 GB, 5.0 TB/s); one token 2.6 us, 256 tokens of a latent cache 6.6 us.  A
 // call of one token among others takes 4.2 us, which is the host's part.
 
-#include "kda_pages.h"
+#include "kda_append_impl.h"
 
 namespace kda {
 namespace {
@@ -31,75 +31,8 @@ struct AppendArgs {
   int64_t q_out_stride;
   kda_rotation rot;
   int32_t units_q, units_k, units;  // units of a token: queries; and keys; and values
+  Axes axes;
 };
-
-typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
-typedef __attribute__((ext_vector_type(2))) float f32x2;
-typedef __attribute__((ext_vector_type(4))) float f32x4;
-
-// NT: non-temporal, for calls that outgrow the caches (see run()).
-template <bool NT, typename V>
-__device__ __forceinline__ V get(const V* p) {
-  return NT ? __builtin_nontemporal_load(p) : *p;
-}
-template <bool NT, typename V>
-__device__ __forceinline__ void put(V* p, const V& x) {
-  if (NT)
-    __builtin_nontemporal_store(x, p);
-  else
-    *p = x;
-}
-
-// 8 values as fp32, and back.
-template <bool NT>
-__device__ __forceinline__ void load8(const bf16_t* p, float (&x)[8]) {
-  const u32x4 w = get<NT>(reinterpret_cast<const u32x4*>(p));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(w[i]);
-    x[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
-template <bool NT>
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const f32x4 w = get<NT>(reinterpret_cast<const f32x4*>(p) + h);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[4 * h + i] = w[i];
-  }
-}
-template <bool NT>
-__device__ __forceinline__ void store8(bf16_t* p, const float (&x)[8]) {
-  u32x4 w;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x[2 * i], x[2 * i + 1]}, bf16x2));
-  put<NT>(reinterpret_cast<u32x4*>(p), w);
-}
-template <bool NT>
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  put<NT>(reinterpret_cast<f32x4*>(p), (f32x4){x[0], x[1], x[2], x[3]});
-  put<NT>(reinterpret_cast<f32x4*>(p) + 1, (f32x4){x[4], x[5], x[6], x[7]});
-}
-
-// e4m3 of x / scale: clamped to the type's largest value (it has no infinity),
-// rounded to nearest even by the conversion.  The division is the IEEE one, so
-// the stored bits are those of the formula.
-__device__ __forceinline__ float to_range(float x, float scale) {
-  const float y = x / scale;
-  return y != y ? y : fminf(fmaxf(y, -448.f), 448.f);
-}
-template <bool NT>
-__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&x)[8], float scale) {
-  int w[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(to_range(x[4 * i], scale), to_range(x[4 * i + 1], scale), w[i], false);
-    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(to_range(x[4 * i + 2], scale), to_range(x[4 * i + 3], scale), w[i], true);
-  }
-  put<NT>(reinterpret_cast<u32x2*>(p), (u32x2){(uint32_t)w[0], (uint32_t)w[1]});
-}
 
 // A sequence with packed row `row` in its range, and which of its tokens that
 // row is; b = -1 for a row of no sequence.
@@ -150,7 +83,7 @@ __device__ __forceinline__ Owner owner_of(const KvBatch& kb, int row, int from, 
 // Unit e to its place for the first sequence from `from` on that has its row
 // (`begin`: see owner_of).
 // Returns where a search for a further one begins, B if there is none.
-template <int DK, int DV, typename TIn, typename TC, bool NT>
+template <int DK, int DV, typename TIn, typename TC, bool NT, bool AXES>
 __device__ __forceinline__ int append_unit(const AppendArgs& a, uint32_t e, int from, int begin) {
   constexpr bool kE4m3 = sizeof(TC) == 1;
   const KvBatch& kb = a.kb;
@@ -165,32 +98,26 @@ __device__ __forceinline__ int append_unit(const AppendArgs& a, uint32_t e, int 
   const bool is_value = u >= a.units_k, is_key = !is_value && u >= a.units_q;
   const bool rotates = a.rot.cos_sin != nullptr;
   const int n_rot = rotates ? a.rot.dim >> 4 : 0;
-  int h, w = 0, c0, c1;
+  int h, w = 0;
+  Chunks c;
   const TIn* src;
   if (is_value) {
     const int at = u - a.units_k;
     h = at / (DV / 16);
-    c0 = at % (DV / 16) * 16;
-    c1 = c0 + 8;
+    c.c0 = at % (DV / 16) * 16;
+    c.c1 = c.c0 + 8;
     src = static_cast<const TIn*>(a.v.p) + row * a.v.stride + h * DV;
   } else {
     const int at = is_key ? u - a.units_q : u;
     h = at / (DK / 16);
     w = at % (DK / 16);
-    if (w < n_rot) {
-      c0 = a.rot.start + (a.rot.pairs ? 16 * w : 8 * w);
-      c1 = c0 + (a.rot.pairs ? 8 : a.rot.dim >> 1);
-    } else {
-      c0 = 16 * (w - n_rot);
-      if (rotates && c0 >= a.rot.start) c0 += a.rot.dim;
-      c1 = c0 + 8;
-    }
+    c = chunks_of(a.rot, n_rot, w);
     src = is_key ? static_cast<const TIn*>(a.k.p) + row * a.k.stride + h * DK
                  : static_cast<const TIn*>(a.q.p) + row * a.q.stride + h * DK;
   }
   float x[8], y[8];
-  load8<NT>(src + c0, x);
-  load8<NT>(src + c1, y);
+  load8<NT>(src + c.c0, x);
+  load8<NT>(src + c.c1, y);
 
   Owner o;
   if (kb.tok_start)
@@ -200,7 +127,13 @@ __device__ __forceinline__ int append_unit(const AppendArgs& a, uint32_t e, int 
   const int b = o.b, next = o.more && (is_key || is_value) ? b + 1 : kb.s.B;
   auto append = [&] {
     const int64_t p = kb.pos[b] + o.token;
-    if (p < 0 || (rotates && p >= a.rot.max_pos)) {
+    bool off = p < 0;
+    AxisPos axis_pos;
+    if constexpr (AXES)
+      axis_pos = axis_positions(a.axes, a.rot, row), off |= axis_pos.bad;
+    else
+      off |= rotates && p >= a.rot.max_pos;
+    if (off) {
       if (u == a.units_q) set_err(kb.dev_err, KDA_DEV_ERR_POS);
       return;
     }
@@ -209,57 +142,42 @@ __device__ __forceinline__ int append_unit(const AppendArgs& a, uint32_t e, int 
     float cc[8], ss[8];
     const bool turn = !is_value && w < n_rot;
     if (turn) {
-      const float* cs = a.rot.cos_sin + p * a.rot.dim + 8 * w;
-      load8<false>(cs, cc);
-      load8<false>(cs + (a.rot.dim >> 1), ss);
+      if constexpr (AXES)
+        angles(a.rot, axis_pos, axes_of_unit<AppendArgs>(w), w, cc, ss);
+      else
+        angles(a.rot, p, w, cc, ss);
     }
     if (page < 0 || page >= kb.pages.n_pages) {
       if (u == a.units_q) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
       return;
     }
 
-    if (turn) {
-      if (a.rot.pairs) {
-        // x holds pairs 0..3 interleaved, y pairs 4..7.
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const float x0 = x[2 * n], x1 = x[2 * n + 1], y0 = y[2 * n], y1 = y[2 * n + 1];
-          x[2 * n] = x0 * cc[n] - x1 * ss[n];
-          x[2 * n + 1] = x1 * cc[n] + x0 * ss[n];
-          y[2 * n] = y0 * cc[4 + n] - y1 * ss[4 + n];
-          y[2 * n + 1] = y1 * cc[4 + n] + y0 * ss[4 + n];
-        }
-      } else {
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const float x0 = x[n], y0 = y[n];
-          x[n] = x0 * cc[n] - y0 * ss[n];
-          y[n] = y0 * cc[n] + x0 * ss[n];
-        }
-      }
-    }
+    if (turn) rotate(x, y, cc, ss, a.rot.pairs);
     if (!is_value && !is_key) {
       TIn* dst = static_cast<TIn*>(a.q_out) + row * a.q_out_stride + h * DK;
-      store8<NT>(dst + c0, x);
-      store8<NT>(dst + c1, y);
+      store8<NT>(dst + c.c0, x);
+      store8<NT>(dst + c.c1, y);
       return;
     }
     const int64_t place = (((int64_t)page * kb.s.Hkv + h) << kb.page_shift) + ((int)p & (kb.pages.page_size - 1));
     TC* dst = is_value ? static_cast<TC*>(kb.pages.v) + place * DV : static_cast<TC*>(kb.pages.k) + place * DK;
     if constexpr (kE4m3) {
       const float scale = (is_value ? kb.pages.v_scale : kb.pages.k_scale)[h];
-      store8_e4m3<NT>(dst + c0, x, scale);
-      store8_e4m3<NT>(dst + c1, y, scale);
+      // The division is the IEEE one, so the stored bits are those of the formula.
+#pragma unroll
+      for (int n = 0; n < 8; ++n) x[n] = x[n] / scale, y[n] = y[n] / scale;
+      store8_e4m3<NT>(dst + c.c0, x);
+      store8_e4m3<NT>(dst + c.c1, y);
     } else {
-      store8<NT>(dst + c0, x);
-      store8<NT>(dst + c1, y);
+      store8<NT>(dst + c.c0, x);
+      store8<NT>(dst + c.c1, y);
     }
   };
   if (live && b >= 0) append();
   return next;
 }
 
-template <int DK, int DV, typename TIn, typename TC, bool NT>
+template <int DK, int DV, typename TIn, typename TC, bool NT, bool AXES>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
   const KvBatch& kb = a.kb;
   // Ranges that do not fit the launch are named by the first block, whether
@@ -272,7 +190,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
   // turn computes is not kept for the next, which took 20 registers (8 prompts of
   // 8192 tokens to e4m3 364 us, now 285).
   for (int from = 0, begin = 0;;) {
-    from = append_unit<DK, DV, TIn, TC, NT>(a, here((int)(blockIdx.x * kThreads + threadIdx.x)), from, begin);
+    from = append_unit<DK, DV, TIn, TC, NT, AXES>(a, here((int)(blockIdx.x * kThreads + threadIdx.x)), from, begin);
     if (__ballot(from < kb.s.B) == 0) return;
     begin = from;
 #pragma unroll
@@ -286,21 +204,26 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
 // 303.  f32 and latent prompts lose by it (16384 f32 tokens 170 us for 147, 32768
 // latent ones 503 for 444).  What smaller calls write stays there for the
 // attention that reads it next.
-template <int DK, int DV, typename TIn, typename TC>
+template <int DK, int DV, typename TIn, typename TC, bool AXES>
 hipError_t run(const AppendArgs& a, hipStream_t st) {
   const int64_t units = (int64_t)a.kb.n_tokens * a.units, blocks = (units + kThreads - 1) / kThreads;
   if (units * 16 * (int64_t)(sizeof(TIn) + sizeof(TC)) > (int64_t)256 << 20)
-    hipLaunchKernelGGL((append_kernel<DK, DV, TIn, TC, true>), dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((append_kernel<DK, DV, TIn, TC, true, AXES>), dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
   else
-    hipLaunchKernelGGL((append_kernel<DK, DV, TIn, TC, false>), dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((append_kernel<DK, DV, TIn, TC, false, AXES>), dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
   return hipGetLastError();
+}
+
+template <int DK, int DV, typename TIn, typename TC>
+hipError_t run(const AppendArgs& a, hipStream_t st) {
+  return a.axes.n ? run<DK, DV, TIn, TC, true>(a, st) : run<DK, DV, TIn, TC, false>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_kv_append(const KvBatch& b, KvRows k, KvRows v, KvRows q, void* q_out, int64_t q_out_stride,
-                            const kda_rotation& rot, hipStream_t st) {
-  AppendArgs a{b, k, v, q, q_out, q_out_stride, rot, 0, 0, 0};
+                            const kda_rotation& rot, const Axes& axes, hipStream_t st) {
+  AppendArgs a{b, k, v, q, q_out, q_out_stride, rot, 0, 0, 0, axes};
   a.units_q = q.p ? b.s.Hq * (b.s.dk / 16) : 0;
   a.units_k = a.units_q + b.s.Hkv * (b.s.dk / 16);
   a.units = a.units_k + (v.p ? b.s.Hkv * (b.s.dv / 16) : 0);
