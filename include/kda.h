@@ -676,7 +676,7 @@ kda_status kda_kv_append_axes(const kda_kv_shape* shape, const kda_pages* pages,
  * Scales of e4m3 pages by blocks of tokens (grouped form, in_dtype KDA_BF16):
  *   k, v   f32 [n_pages][Hkv][page_size / block]: the page's tokens i * block
  *          and on hold value / scale with scale i of their kv head
- *   block  a power of two from 16 to page_size
+ *   block  a power of two from 16 to 256, at most page_size
  * Calls that take these ignore kda_pages.k_scale and v_scale.  The append sets
  * a scale to a power of two, so that dividing by it loses nothing.  The
  * attention takes any scales.

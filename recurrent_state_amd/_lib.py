@@ -780,8 +780,8 @@ def _scales(pool):
 def _check_scale_block(block, page_size, dtype, latent):
     if dtype != torch.float8_e4m3fn or latent:
         raise ValueError("scales by blocks belong to float8_e4m3fn pages of keys and values")
-    if block < 16 or block > page_size or block & (block - 1):
-        raise ValueError(f"scale_block is {block}, expected a power of two from 16 to the page size")
+    if block < 16 or block > min(page_size, 256) or block & (block - 1):
+        raise ValueError(f"scale_block is {block}, expected a power of two from 16 to 256, at most the page size")
 
 
 def _need_gpu(t, name):

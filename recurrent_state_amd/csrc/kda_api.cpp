@@ -189,7 +189,7 @@ kda_status check_scales(const kda_kv_shape& s, const kda_pages& pages, const kda
   if (!scales) return KDA_ERR_NULL;
   if (s.cache_dtype != KDA_E4M3) return KDA_ERR_DTYPE;
   const int32_t n = scales->block;
-  if (n < 16 || n > pages.page_size || (n & (n - 1)) != 0) return KDA_ERR_SHAPE;
+  if (n < 16 || n > 256 || n > pages.page_size || (n & (n - 1)) != 0) return KDA_ERR_SHAPE;
   if (!empty && (!scales->k || !scales->v)) return KDA_ERR_NULL;
   if (!aligned(scales->k, 4) || !aligned(scales->v, 4)) return KDA_ERR_ALIGN;
   int32_t shift = 0;

@@ -12,10 +12,13 @@ typedef __attribute__((ext_vector_type(4))) uint32_t codes16;  // 16 e4m3 values
 
 constexpr uint32_t kLeastScale = (127u - 64) << 23, kMostScale = (127u + 120) << 23;  // 2^-64, 2^120
 
-// |x| as bits, which order as the values do; 0 for what is not finite.
+// |x| as bits, which order as the values do, infinities and then NaN behind
+// kLargest; and with 0 for what is not finite.
+constexpr uint32_t kLargest = 0x7f7fffffu;
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 __device__ __forceinline__ uint32_t finite_bits(float x) {
-  const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
-  return b < 0x7f800000u ? b : 0;
+  const uint32_t b = magnitude(x);
+  return b <= kLargest ? b : 0;
 }
 // The bits of the least power of two s >= 2^-64 with m <= 448 s, m given by its
 // bits: 448 = 1.75 * 2^8, so with m = f * 2^x the exponent is x - 8, one more where

@@ -30,34 +30,195 @@ struct EvictArgs {
   int32_t* kept;
 };
 
-constexpr int kSelect = 1024, kSelectWaves = kSelect / kWave, kBins = 2048;
+constexpr int kSelect = 1024, kSelectWaves = kSelect / kWave, kBins = 2048, kList = 8192;
+constexpr int kShort = 8 * kSelect;  // candidates that a workgroup holds in registers
 
 // Numbers that order as the weights do: NaN first, -0 and 0 alike.
 __device__ __forceinline__ uint32_t order(float w) {
   const uint32_t u = __float_as_uint(w + 0.f);
-  return w != w ? 0u : (u >> 31) ? ~u : u | 0x80000000u;
+  return w != w ? 0u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-// Inclusive sum over the workgroup's threads.
-__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* lds) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const uint32_t upto = (uint32_t)wave_scan((int32_t)x);
-  __syncthreads();
-  if (lane == kWave - 1) lds[wave] = upto;
-  __syncthreads();
-  uint32_t before = 0;
-#pragma unroll
-  for (int i = 0; i < kSelectWaves; ++i) before += i < wave ? lds[i] : 0;
-  return before + upto;
+// How many lanes of a mask come before this one, added to `n`.
+__device__ __forceinline__ uint32_t lanes_before(uint64_t mask, uint32_t n) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, n));
 }
 
-__global__ void __launch_bounds__(kSelect) select_kernel(EvictArgs a) {
-  __shared__ uint32_t hist[kBins];
-  __shared__ uint32_t lds_scan[kSelectWaves];
-  __shared__ uint32_t found[2];  // the digit, and how many keys are above it
-  __shared__ uint2 counts[kSelectWaves];
-  const KvBatch& kb = a.kb;
+struct SelectLds {
+  uint32_t hist[kBins];
+  uint32_t scan[kSelectWaves];
+  uint32_t found[3];           // the digit, how many keys are above it, and how many have it
+  uint32_t gt[kSelectWaves], eq[kSelectWaves];  // of each wave's candidates, above the threshold and at it
+  uint32_t length;
+  uint32_t list[kList];        // keys that share the first digit
+  uint8_t wave[kList];         // and whose candidates they are
+};
+
+// The digit of the k-th greatest key, from the histogram of `bins` digits and the
+// count of keys above them all; sets lds.found.
+__device__ __forceinline__ void find_digit(SelectLds& lds, uint32_t above, uint32_t k) {
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  __syncthreads();
+  // From the greatest digit down, two to a thread.
+  const int d0 = kBins - 1 - 2 * tid;
+  const uint32_t c0 = lds.hist[d0], c1 = lds.hist[d0 - 1];
+  uint32_t upto = (uint32_t)wave_scan((int32_t)(c0 + c1));
+  if (lane == kWave - 1) lds.scan[wave] = upto;
+  __syncthreads();
+  upto += above;
+#pragma unroll
+  for (int i = 0; i < kSelectWaves; ++i) upto += i < wave ? lds.scan[i] : 0;
+  const uint32_t before = upto - c0 - c1;
+  if (before < k && upto >= k) {  // one thread
+    const bool second = before + c0 < k;
+    lds.found[0] = second ? d0 - 1 : d0;
+    lds.found[1] = second ? before + c0 : before;
+    lds.found[2] = second ? c1 : c0;
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ void clear_hist(SelectLds& lds) {
+  __syncthreads();
+  lds.hist[threadIdx.x] = 0, lds.hist[threadIdx.x + kSelect] = 0;
+  __syncthreads();
+}
+
+// The k greatest of n weights, 0 < k < n: their places to kept, in order, and the
+// weights to out_w.  A wave has a stretch of neighbours, 64 at a time.  V: a
+// thread's share, held in registers; 0: more than that, read again for every
+// pass, kBatch at once.
+template <int V>
+__device__ __forceinline__ void select(const float* w, int n, int k, int32_t* kept, float* out_w, SelectLds& lds) {
+  constexpr int kBatch = 16;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int each = V > 0 ? V * kWave : (n + kSelect * kBatch - 1) / (kSelect * kBatch) * (kWave * kBatch);
+  const int j0 = wave * each, j1 = min(j0 + each, n);  // j1 <= j0: nothing
+  float held[V > 0 ? V : 1];
+  if constexpr (V > 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int j = j0 + i * kWave + lane;
+      held[i] = j < j1 ? w[j] : 0.f;
+    }
+  }
+  // f(place, weight, whether it is there) for the wave's stretch, by whole waves.
+  auto all = [&](auto f) __attribute__((always_inline)) {
+    if constexpr (V > 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int j = j0 + i * kWave;
+        if (j < j1) f(j + lane, held[i], j + lane < j1);
+      }
+    } else {
+      for (int at = j0; at < j1; at += kWave * kBatch) {
+        float x[kBatch];
+        if (at + kWave * kBatch <= j1) {
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) x[i] = w[at + i * kWave + lane];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) f(at + i * kWave + lane, x[i], true);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int j = at + i * kWave + lane;
+            x[i] = j < j1 ? w[j] : 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            if (at + i * kWave < j1) f(at + i * kWave + lane, x[i], at + i * kWave + lane < j1);
+        }
+      }
+    }
+  };
+
+  // The threshold, digit by digit, and how many keys are above it.
+  clear_hist(lds);
+  all([&](int, float x, bool there) {
+    if (there) atomicAdd(&lds.hist[order(x) >> 21], 1u);
+  });
+  find_digit(lds, 0, k);
+  uint32_t top = lds.found[0], above = lds.found[1];
+  const bool listed = V == 0 && lds.found[2] <= kList;
+  if (tid == 0) lds.length = 0;
+  if (tid < kSelectWaves) lds.gt[tid] = lds.eq[tid] = 0;
+  if (listed) {
+    // The keys with that digit fit a list; the others need not be looked at for
+    // what is left of the threshold.
+    __syncthreads();
+    const uint32_t digit = top;
+    uint32_t gt = 0;
+    all([&](int, float x, bool there) {
+      const uint32_t key = order(x);
+      gt += __popcll(__ballot(there && key >> 21 > digit));
+      const bool in = there && key >> 21 == digit;
+      const uint64_t mask = __ballot(in);
+      if (mask == 0) return;
+      uint32_t at = 0;
+      if (lane == 0) at = atomicAdd(&lds.length, (uint32_t)__popcll(mask));
+      at = lanes_before(mask, __builtin_amdgcn_readfirstlane(at));
+      if (in) lds.list[at] = key, lds.wave[at] = wave;
+    });
+    if (lane == 0) lds.gt[wave] = gt;
+  }
+#pragma unroll
+  for (int pass = 1; pass < 3; ++pass) {
+    const int shift = pass == 1 ? 10 : 0, bits = pass == 1 ? 11 : 10;
+    clear_hist(lds);
+    if (listed) {
+      for (uint32_t i = tid; i < lds.length; i += kSelect)
+        if (lds.list[i] >> (shift + bits) == top) atomicAdd(&lds.hist[lds.list[i] >> shift & ((1u << bits) - 1)], 1u);
+    } else {
+      all([&](int, float x, bool there) {
+        const uint32_t key = order(x);
+        if (there && key >> (shift + bits) == top) atomicAdd(&lds.hist[key >> shift & ((1u << bits) - 1)], 1u);
+      });
+    }
+    find_digit(lds, above, k);
+    top = top << bits | lds.found[0];
+    above = lds.found[1];
+  }
+  const uint32_t equal = (uint32_t)k - above;  // of those at the threshold, the first so many
+
+  // How many of the waves before this one's are kept, then which of its own.
+  if (listed) {
+    for (uint32_t i = tid; i < lds.length; i += kSelect) {
+      const uint32_t key = lds.list[i];
+      if (key >= top) atomicAdd(key > top ? &lds.gt[lds.wave[i]] : &lds.eq[lds.wave[i]], 1u);
+    }
+  } else {
+    uint32_t gt = 0, eq = 0;
+    all([&](int, float x, bool there) {
+      const uint32_t key = order(x);
+      gt += __popcll(__ballot(there && key > top));
+      eq += __popcll(__ballot(there && key == top));
+    });
+    if (lane == 0) lds.gt[wave] = gt, lds.eq[wave] = eq;
+  }
+  __syncthreads();
+  uint32_t gt = 0, eq = 0;
+#pragma unroll
+  for (int i = 0; i < kSelectWaves; ++i) gt += i < wave ? lds.gt[i] : 0, eq += i < wave ? lds.eq[i] : 0;
+  gt = __builtin_amdgcn_readfirstlane(gt), eq = __builtin_amdgcn_readfirstlane(eq);
+  all([&](int j, float x, bool there) {
+    const uint32_t key = order(x);
+    const uint64_t is_gt = __ballot(there && key > top), is_eq = __ballot(there && key == top);
+    const uint32_t e = lanes_before(is_eq, eq);
+    if (there && (key > top || (key == top && e < equal))) {
+      const uint32_t at = lanes_before(is_gt, gt) + min(e, equal);
+      kept[at] = j;
+      out_w[at] = x;
+    }
+    gt += __popcll(is_gt);
+    eq += __popcll(is_eq);
+  });
+}
+
+// LONG: rows may have more than kShort candidates.
+template <bool LONG>
+__global__ void __launch_bounds__(kSelect, LONG ? 4 : 8) select_kernel(EvictArgs a) {
+  __shared__ SelectLds lds;
+  const KvBatch& kb = a.kb;
+  const int tid = threadIdx.x;
   const int b = blockIdx.x / kb.s.Hkv;
   const float* const w = a.weights + (int64_t)blockIdx.x * a.stride;
   float* const out_w = a.new_weights + (int64_t)blockIdx.x * a.stride;
@@ -83,68 +244,13 @@ __global__ void __launch_bounds__(kSelect) select_kernel(EvictArgs a) {
     return;
   }
 
-  // The threshold: of the n candidates' keys the k-th greatest, and how many are above.
+  // The n candidates, of which the k greatest are kept.
   const int n = L - a.recent, k = a.keep - a.recent;
-  uint32_t top = 0, above = 0;  // digits so far; keys greater than any with these
   if (k > 0) {
-    constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
-#pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = kShift[pass];
-      const uint32_t mask = (1u << kBits[pass]) - 1;
-      hist[tid] = 0, hist[tid + kSelect] = 0;
-      __syncthreads();
-#pragma unroll 4
-      for (int j = tid; j < n; j += kSelect) {
-        const uint32_t key = order(w[j]);
-        if (pass == 0 || key >> (shift + kBits[pass]) == top) atomicAdd(&hist[key >> shift & mask], 1u);
-      }
-      __syncthreads();
-      // From the greatest digit down, two to a thread.
-      const int d0 = kBins - 1 - 2 * tid;
-      const uint32_t c0 = hist[d0], c1 = hist[d0 - 1], upto = block_scan(c0 + c1, lds_scan) + above;
-      const uint32_t before = upto - c0 - c1;
-      if (before < (uint32_t)k && upto >= (uint32_t)k) {  // one thread
-        const bool second = before + c0 < (uint32_t)k;
-        found[0] = second ? d0 - 1 : d0;
-        found[1] = second ? before + c0 : before;
-      }
-      __syncthreads();
-      top = top << kBits[pass] | found[0];
-      above = found[1];
-    }
-  }
-  const uint32_t equal = k > 0 ? (uint32_t)k - above : 0;  // of those at the threshold, the first so many
-
-  // Each wave's stretch of the candidates.
-  const int each = (n + kSelect - 1) / kSelect * kWave, j0 = min(wave * each, n), j1 = min(j0 + each, n);
-  if (k > 0) {
-    uint32_t gt = 0, eq = 0;
-#pragma unroll 4
-    for (int j = j0 + lane; j - lane < j1; j += kWave) {
-      const uint32_t key = j < j1 ? order(w[j]) : 0;
-      gt += __popcll(__ballot(j < j1 && key > top));
-      eq += __popcll(__ballot(j < j1 && key == top));
-    }
-    if (lane == 0) counts[wave] = make_uint2(gt, eq);
-    __syncthreads();
-    gt = eq = 0;
-    for (int i = 0; i < wave; ++i) gt += counts[i].x, eq += counts[i].y;
-    const uint64_t below = ((uint64_t)1 << lane) - 1;
-#pragma unroll 4
-    for (int j = j0 + lane; j - lane < j1; j += kWave) {
-      const float x = j < j1 ? w[j] : 0.f;
-      const uint32_t key = order(x);
-      const uint64_t is_gt = __ballot(j < j1 && key > top), is_eq = __ballot(j < j1 && key == top);
-      const uint32_t g = gt + __popcll(is_gt & below), e = eq + __popcll(is_eq & below);
-      if (j < j1 && (key > top || (key == top && e < equal))) {
-        const uint32_t at = g + min(e, equal);
-        kept[at] = j;
-        out_w[at] = x;
-      }
-      gt += __popcll(is_gt);
-      eq += __popcll(is_eq);
-    }
+    if (!LONG || n <= kShort)
+      select<kShort / kSelect>(w, n, k, kept, out_w, lds);
+    else
+      select<0>(w, n, k, kept, out_w, lds);
   }
   for (int i = tid; i < a.recent; i += kSelect) {
     kept[k + i] = n + i;
@@ -165,119 +271,155 @@ __device__ __forceinline__ void set_length(const EvictArgs& a, int b) {
 
 constexpr int kMove = 256;
 
-// Rows of `units` 16-byte units.  Workgroups (b, part) by x; y: kv heads, of keys and then of values.
+// Rows of `units` 16-byte units, keys and values together.  Workgroups (b, part) by x; kv heads by y.
+template <bool VALUES>
 __global__ void __launch_bounds__(kMove) move_kernel(EvictArgs a, int units, int parts) {
+  constexpr int kAtOnce = 4;
   const KvBatch& kb = a.kb;
-  const int b = blockIdx.x / parts, part = blockIdx.x % parts;
-  const bool values = (int)blockIdx.y >= kb.s.Hkv;
-  const int h = values ? blockIdx.y - kb.s.Hkv : blockIdx.y;
-  if (part == 0 && blockIdx.y == 0) set_length(a, b);
+  const int b = blockIdx.x / parts, part = blockIdx.x % parts, h = blockIdx.y;
+  if (part == 0 && h == 0) set_length(a, b);
   const int32_t* const kept = a.kept + ((int64_t)b * kb.s.Hkv + h) * a.keep;
   if (kept[0] < 0) return;
-  u32x4* const pool = static_cast<u32x4*>(values ? kb.pages.v : kb.pages.k);
+  u32x4* const k = static_cast<u32x4*>(kb.pages.k);
+  u32x4* const v = static_cast<u32x4*>(kb.pages.v);
   const int32_t* const from = kb.table + (int64_t)b * kb.max_pages;
   const int32_t* const to = a.dst_table + (int64_t)b * a.dst_max_pages;
   const int64_t total = (int64_t)a.keep * units;
-#pragma unroll 4
-  for (int64_t x = (int64_t)part * kMove + threadIdx.x; x < total; x += (int64_t)parts * kMove) {
-    const int i = (int)(x / units), c = (int)(x - (int64_t)i * units);
-    pool[row_at(kb, to, h, i) * units + c] = pool[row_at(kb, from, h, kept[i]) * units + c];
+  for (int64_t x0 = (int64_t)part * (kMove * kAtOnce) + threadIdx.x; x0 < total; x0 += (int64_t)parts * (kMove * kAtOnce)) {
+    u32x4 xk[kAtOnce], xv[kAtOnce];
+    int64_t dst[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int64_t x = x0 + u * kMove;
+      dst[u] = -1;
+      if (x >= total) continue;
+      const int i = (int)(x / units), c = (int)(x - (int64_t)i * units);
+      const int64_t src = row_at(kb, from, h, kept[i]) * units + c;
+      xk[u] = k[src];
+      if (VALUES) xv[u] = v[src];
+      dst[u] = row_at(kb, to, h, i) * units + c;
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      if (dst[u] < 0) continue;
+      k[dst[u]] = xk[u];
+      if (VALUES) v[dst[u]] = xv[u];
+    }
   }
 }
 
-// W waves to a new block of one kv head; NW waves to a workgroup.
-template <int D, int W>
+// Rows of one side of a new block in a wave's registers: 16 values of a row to a lane.
+template <int PASSES>
+struct Held {
+  codes16 x[PASSES];
+  float scale[PASSES];  // 0 for a row that is not there
+
+  __device__ __forceinline__ void load(int p, const void* pool, const float* scales, int64_t row, int64_t at, int shift) {
+    x[p] = *reinterpret_cast<const codes16*>(static_cast<const uint8_t*>(pool) + at);
+    scale[p] = scales[row >> shift];
+  }
+  // The largest finite magnitude, as bits.  Among codes: one more than the
+  // magnitude's, which orders as the values do and sends NaN (0x7f) to 0; two
+  // bytes at a time.
+  __device__ __forceinline__ uint32_t top() const {
+    typedef __attribute__((ext_vector_type(2))) uint16_t u16x2;
+    uint32_t m = 0;
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      u16x2 most = {0, 0};
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const uint32_t y = ((x[p][n] & 0x7f7f7f7fu) + 0x01010101u) & 0x7f7f7f7fu;
+        most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, y & 0x00ff00ffu));
+        most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, y >> 8 & 0x00ff00ffu));
+      }
+      const int code = max((int)most[0], (int)most[1]);
+      const float value = code ? __builtin_amdgcn_cvt_f32_fp8(code - 1, 0) : 0.f;
+      m = max(m, finite_bits(value * scale[p]));
+    }
+    return m;
+  }
+};
+
+// A wave takes up to 32 rows of a new block, keys and values together, so that many
+// loads are on their way; W waves to a block, NW to a workgroup.
+template <int D, int ROWS, int W>
 __global__ void __launch_bounds__(64 * (W > 4 ? W : 4)) move_blocks_kernel(EvictArgs a, int parts) {
-  constexpr int NW = W > 4 ? W : 4, HELD = NW / W;
-  constexpr int LPR = D / 16, RPP = kWave / LPR, PASSES = 16 / RPP;
-  __shared__ uint32_t lds_max[NW];
+  constexpr int NW = W > 4 ? W : 4, BLOCKS = NW / W, SHIFT = __builtin_ctz(ROWS * W);
+  constexpr int LPR = D / 16, RPP = kWave / LPR, PASSES = ROWS / RPP;
+  __shared__ uint2 lds_max[NW];
   const KvBatch& kb = a.kb;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63, group = wave % W;
-  const int b = blockIdx.x / parts, part = blockIdx.x % parts;
-  const bool values = (int)blockIdx.y >= kb.s.Hkv;
-  const int h = values ? blockIdx.y - kb.s.Hkv : blockIdx.y;
-  if (part == 0 && blockIdx.y == 0) set_length(a, b);
+  const int b = blockIdx.x / parts, part = blockIdx.x % parts, h = blockIdx.y;
+  if (part == 0 && h == 0) set_length(a, b);
   const int32_t* const kept = a.kept + ((int64_t)b * kb.s.Hkv + h) * a.keep;
   if (kept[0] < 0) return;
-  uint8_t* const pool = static_cast<uint8_t*>(values ? kb.pages.v : kb.pages.k);
-  float* const scales = values ? a.scales.v : a.scales.k;
   const int32_t* const from = kb.table + (int64_t)b * kb.max_pages;
   const int32_t* const to = a.dst_table + (int64_t)b * a.dst_max_pages;
-  const int shift = a.scales.shift, blocks = (a.keep + (1 << shift) - 1) >> shift;
-  for (int at = part * HELD; at < blocks; at += parts * HELD) {
-    const int block = at + wave / W;
-    const int begin = block << shift, count = block < blocks ? min(a.keep - begin, 1 << shift) : 0;
-    codes16 x[PASSES];
-    float was[PASSES];
-    uint32_t m = 0;
-    auto load = [&](int first) __attribute__((always_inline)) {
+  const int blocks = (a.keep + (1 << SHIFT) - 1) >> SHIFT, column = 16 * (lane % LPR);
+  for (int at = part * BLOCKS; at < blocks; at += parts * BLOCKS) {
+    const int block = at + wave / W, begin = block << SHIFT;
+    const int count = block < blocks ? min(a.keep - begin, 1 << SHIFT) : 0;
+    const int first = group * ROWS + lane / LPR;  // this lane's rows: every RPP-th from here on
+    int64_t src[PASSES];
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        const int i = first + group * 16 + p * RPP + lane / LPR;
-        x[p] = codes16{};
-        was[p] = 0.f;
-        if (i >= count) continue;
-        const int64_t row = row_at(kb, from, h, kept[begin + i]);
-        x[p] = *reinterpret_cast<const codes16*>(pool + row * D + 16 * (lane % LPR));
-        was[p] = scales[row >> shift];
-      }
-    };
-    for (int first = 0; first < 1 << shift; first += 16 * W) {
-      load(first);
+    for (int p = 0; p < PASSES; ++p) src[p] = first + p * RPP < count ? kept[begin + first + p * RPP] : 0;
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p)
+    for (int p = 0; p < PASSES; ++p) src[p] = row_at(kb, from, h, (int)src[p]);
+    Held<PASSES> k, v;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[p][n], false);
-          const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[p][n], true);
-          m = max(max(m, max(finite_bits(lo[0] * was[p]), finite_bits(lo[1] * was[p]))),
-                  max(finite_bits(hi[0] * was[p]), finite_bits(hi[1] * was[p])));
-        }
+    for (int p = 0; p < PASSES; ++p) {
+      k.load(p, kb.pages.k, a.scales.k, src[p], src[p] * D + column, SHIFT);
+      v.load(p, kb.pages.v, a.scales.v, src[p], src[p] * D + column, SHIFT);
+      if (first + p * RPP >= count) k.scale[p] = v.scale[p] = 0.f;
     }
-    m = wave_max(m);
+    uint32_t mk = wave_max(k.top()), mv = wave_max(v.top());
     if (W > 1) {
       __syncthreads();
-      if (lane == 0) lds_max[wave] = m;
+      if (lane == 0) lds_max[wave] = make_uint2(mk, mv);
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < W; ++i) m = max(m, lds_max[wave - group + i]);
+      for (int i = 0; i < W; ++i) mk = max(mk, lds_max[wave - group + i].x), mv = max(mv, lds_max[wave - group + i].y);
     }
-    const uint32_t s = scale_for(m);
-    const int64_t dst = count > 0 ? row_at(kb, to, h, begin) : 0;
-    if (count > 0 && group == 0 && lane == 0) scales[dst >> shift] = __uint_as_float(s);
-    for (int first = 0; first < 1 << shift; first += 16 * W) {
-      if (1 << shift > 16 * W) load(first);
+    if (count == 0) continue;
+    const uint32_t sk = scale_for(mk), sv = scale_for(mv);
+    const int64_t dst = row_at(kb, to, h, begin);
+    if (group == 0 && lane == 0) {
+      a.scales.k[dst >> SHIFT] = __uint_as_float(sk);
+      a.scales.v[dst >> SHIFT] = __uint_as_float(sv);
+    }
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        const int i = first + group * 16 + p * RPP + lane / LPR;
-        if (i < count)
-          *reinterpret_cast<codes16*>(pool + (dst + i) * D + 16 * (lane % LPR)) = rescaled(x[p], was[p] * inverse(s));
-      }
+    for (int p = 0; p < PASSES; ++p) {
+      const int i = first + p * RPP;
+      if (i >= count) continue;
+      const int64_t to_at = (dst + i) * D + column;
+      *reinterpret_cast<codes16*>(static_cast<uint8_t*>(kb.pages.k) + to_at) = rescaled(k.x[p], k.scale[p] * inverse(sk));
+      *reinterpret_cast<codes16*>(static_cast<uint8_t*>(kb.pages.v) + to_at) = rescaled(v.x[p], v.scale[p] * inverse(sv));
     }
   }
 }
 
-template <int D, int W>
+template <int D, int ROWS, int W>
 hipError_t run_blocks(const EvictArgs& a, hipStream_t st) {
   constexpr int NW = W > 4 ? W : 4;
-  const int blocks = (a.keep + (1 << a.scales.shift) - 1) >> a.scales.shift;
-  const int64_t groups = (int64_t)a.kb.s.B * a.kb.s.Hkv * 2;
+  const int blocks = (a.keep + ROWS * W - 1) / (ROWS * W);
+  const int64_t groups = (int64_t)a.kb.s.B * a.kb.s.Hkv;
   int64_t parts = (blocks + NW / W - 1) / (NW / W);
   const int64_t most = (((int64_t)1 << 32) - 1) / (groups * NW * kWave);  // threads of a launch
-  if (parts > most) parts = most < 1 ? 1 : most;
-  hipLaunchKernelGGL((move_blocks_kernel<D, W>), dim3((unsigned)(a.kb.s.B * parts), a.kb.s.Hkv * 2), dim3(NW * kWave), 0,
-                     st, a, (int)parts);
+  if (parts > most) parts = most;
+  hipLaunchKernelGGL((move_blocks_kernel<D, ROWS, W>), dim3((unsigned)(a.kb.s.B * parts), a.kb.s.Hkv), dim3(NW * kWave),
+                     0, st, a, (int)parts);
   return hipGetLastError();
 }
 template <int D>
 hipError_t by_block(const EvictArgs& a, hipStream_t st) {
   switch (a.scales.shift) {
-    case 4: return run_blocks<D, 1>(a, st);
-    case 5: return run_blocks<D, 2>(a, st);
-    case 6: return run_blocks<D, 4>(a, st);
-    case 7: return run_blocks<D, 8>(a, st);
+    case 4: return run_blocks<D, 16, 1>(a, st);
+    case 5: return run_blocks<D, 32, 1>(a, st);
+    case 6: return run_blocks<D, 32, 2>(a, st);
+    case 7: return run_blocks<D, 32, 4>(a, st);
   }
-  return run_blocks<D, 16>(a, st);
+  return run_blocks<D, 32, 8>(a, st);
 }
 
 }  // namespace
@@ -287,17 +429,24 @@ hipError_t launch_kv_evict(const KvBatch& b, const BlockScales& scales, const fl
                            int64_t* new_len, float* new_weights, int32_t* kept, hipStream_t st) {
   const EvictArgs a{b, scales, weights, stride, keep, recent, dst_table, dst_max_pages, new_len, new_weights, kept};
   const kda_kv_shape& s = b.s;
-  hipLaunchKernelGGL(select_kernel, dim3((unsigned)(s.B * s.Hkv)), dim3(kSelect), 0, st, a);
-  hipError_t e = hipGetLastError();
+  const dim3 rows((unsigned)(s.B * s.Hkv));
+  if (((int64_t)b.max_pages << b.page_shift) > kShort)
+    hipLaunchKernelGGL((select_kernel<true>), rows, dim3(kSelect), 0, st, a);
+  else
+    hipLaunchKernelGGL((select_kernel<false>), rows, dim3(kSelect), 0, st, a);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (scales.k) return s.dk == 128 ? by_block<128>(a, st) : by_block<64>(a, st);
   const int es = s.cache_dtype == KDA_F32 ? 4 : s.cache_dtype == KDA_BF16 ? 2 : 1;
-  const int units = s.dk * es / 16, sides = b.pages.v ? 2 : 1;
+  const int units = s.dk * es / 16;
   int64_t parts = ((int64_t)keep * units + 4 * kMove - 1) / (4 * kMove);
-  const int64_t most = (((int64_t)1 << 32) - 1) / ((int64_t)s.B * s.Hkv * sides * kMove);
-  if (parts > most) parts = most < 1 ? 1 : most;
-  hipLaunchKernelGGL(move_kernel, dim3((unsigned)(s.B * parts), s.Hkv * sides), dim3(kMove), 0, st, a, units,
-                     (int)parts);
+  const int64_t most = (((int64_t)1 << 32) - 1) / ((int64_t)s.B * s.Hkv * kMove);
+  if (parts > most) parts = most;
+  const dim3 grid((unsigned)(s.B * parts), s.Hkv);
+  if (b.pages.v)
+    hipLaunchKernelGGL((move_kernel<true>), grid, dim3(kMove), 0, st, a, units, (int)parts);
+  else
+    hipLaunchKernelGGL((move_kernel<false>), grid, dim3(kMove), 0, st, a, units, (int)parts);
   return hipGetLastError();
 }
 

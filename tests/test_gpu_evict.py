@@ -120,7 +120,7 @@ def test_budgets(kda, form, keep):
     c.check(recent)
 
 
-@pytest.mark.parametrize("block,page", [(16, 1024), (64, 64), (128, 256), (256, 256), (512, 1024), (1024, 1024)])
+@pytest.mark.parametrize("block,page", [(16, 1024), (64, 64), (128, 256), (256, 256), (256, 1024), (32, 512)])
 def test_blocks(kda, block, page):
     c = Cut("blocks_d128", [3000, 1500], 1100, page=page, block=block, seed=block)
     c.run(kda, 100)

@@ -111,6 +111,8 @@ def test_block_scales(k, f):  # noqa: F811
     e4 = shp(k, ct=E4M3)
     for block in (0, 8, 24, 128, -64, 1 << 30):
         assert f(k, e4, sc=scales(k, block=block)) == SHAPE
+    assert f(k, e4, pages(k, size=1024), sc=scales(k, block=512), **({"keep": 9} if f is evict else {}),
+             **({"stride": 1 << 12} if f in (weigh, evict) else {})) == SHAPE
     assert f(k, e4, sc=scales(k, ks=None)) == NULL and f(k, e4, sc=scales(k, vs=None)) == NULL
     assert f(k, e4, sc=scales(k, ks=0x10002)) == ALIGN
     assert f(k, shp(k), sc=scales(k)) == DTYPE and f(k, shp(k, dt=F32, ct=F32), sc=scales(k)) == DTYPE
