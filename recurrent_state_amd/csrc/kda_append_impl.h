@@ -62,13 +62,24 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
 // 8 values as e4m3: clamped to the type's largest (it has no infinity; NaN stays
 // NaN) and rounded to nearest even by the conversion.
 __device__ __forceinline__ float to_range(float y) { return y != y ? y : fminf(fmaxf(y, -448.f), 448.f); }
-template <bool NT>
-__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&y)[8]) {
+__device__ __forceinline__ u32x2 e4m3_of(const float (&y)[8]) {  // of values in range
   int w[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(to_range(y[4 * i]), to_range(y[4 * i + 1]), w[i], false);
-    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(to_range(y[4 * i + 2]), to_range(y[4 * i + 3]), w[i], true);
+    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], w[i], false);
+    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], w[i], true);
+  }
+  return (u32x2){(uint32_t)w[0], (uint32_t)w[1]};
+}
+// x / scale so; the division is the IEEE one, so the stored bits are those of the
+// formula.
+template <bool NT>
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&x)[8], float scale) {
+  int w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(to_range(x[4 * i] / scale), to_range(x[4 * i + 1] / scale), w[i], false);
+    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(to_range(x[4 * i + 2] / scale), to_range(x[4 * i + 3] / scale), w[i], true);
   }
   put<NT>(reinterpret_cast<u32x2*>(p), (u32x2){(uint32_t)w[0], (uint32_t)w[1]});
 }

@@ -7,7 +7,10 @@
 // (n, dim / 2 + n), neighbours for (2n, 2n + 1) and for values that are not
 // rotated), so nothing is exchanged between lanes and q_out may be q itself.
 // A token's units are numbered queries, keys, values; consecutive threads take
-// consecutive units, so a wave covers whole 128-byte lines of a head row.
+// consecutive units, so a wave covers whole 128-byte lines of a head row.  With
+// positions on several axes the cosines and sines of a unit may come from as many
+// rows of the table, pair by pair; in large calls a thread reads them once for
+// the same unit of four heads.
 //
 // Bound by memory for prompts, and by the chain of dependent loads (token range,
 // position, page) for a few tokens: the unit's values depend on none of these
@@ -30,7 +33,7 @@ struct AppendArgs {
   void* q_out;
   int64_t q_out_stride;
   kda_rotation rot;
-  int32_t units_q, units_k, units;  // units of a token: queries; and keys; and values
+  int32_t units_q, units_k, units;  // threads of a token: for queries; and keys; and values
   Axes axes;
 };
 
@@ -80,10 +83,10 @@ __device__ __forceinline__ Owner owner_of(const KvBatch& kb, int row, int from, 
   return o;
 }
 
-// Unit e to its place for the first sequence from `from` on that has its row
+// Unit e, of HEADS heads, to its place for the first sequence from `from` on that has its row
 // (`begin`: see owner_of).
 // Returns where a search for a further one begins, B if there is none.
-template <int DK, int DV, typename TIn, typename TC, bool NT, bool AXES>
+template <int DK, int DV, typename TIn, typename TC, bool NT, bool AXES, int HEADS>
 __device__ __forceinline__ int append_unit(const AppendArgs& a, uint32_t e, int from, int begin) {
   constexpr bool kE4m3 = sizeof(TC) == 1;
   const KvBatch& kb = a.kb;
@@ -103,21 +106,26 @@ __device__ __forceinline__ int append_unit(const AppendArgs& a, uint32_t e, int 
   const TIn* src;
   if (is_value) {
     const int at = u - a.units_k;
-    h = at / (DV / 16);
+    h = at / (DV / 16) * HEADS;
     c.c0 = at % (DV / 16) * 16;
     c.c1 = c.c0 + 8;
     src = static_cast<const TIn*>(a.v.p) + row * a.v.stride + h * DV;
   } else {
     const int at = is_key ? u - a.units_q : u;
-    h = at / (DK / 16);
+    h = at / (DK / 16) * HEADS;
     w = at % (DK / 16);
     c = chunks_of(a.rot, n_rot, w);
     src = is_key ? static_cast<const TIn*>(a.k.p) + row * a.k.stride + h * DK
                  : static_cast<const TIn*>(a.q.p) + row * a.q.stride + h * DK;
   }
-  float x[8], y[8];
-  load8<NT>(src + c.c0, x);
-  load8<NT>(src + c.c1, y);
+  const int width = is_value ? DV : DK, heads = HEADS == 1 ? 1 : min(HEADS, (is_key || is_value ? kb.s.Hkv : kb.s.Hq) - h);
+  float x[HEADS][8], y[HEADS][8];
+#pragma unroll
+  for (int i = 0; i < HEADS; ++i)
+    if (i < heads) {
+      load8<NT>(src + i * width + c.c0, x[i]);
+      load8<NT>(src + i * width + c.c1, y[i]);
+    }
 
   Owner o;
   if (kb.tok_start)
@@ -152,32 +160,40 @@ __device__ __forceinline__ int append_unit(const AppendArgs& a, uint32_t e, int 
       return;
     }
 
-    if (turn) rotate(x, y, cc, ss, a.rot.pairs);
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i)
+      if (turn && i < heads) rotate(x[i], y[i], cc, ss, a.rot.pairs);
     if (!is_value && !is_key) {
       TIn* dst = static_cast<TIn*>(a.q_out) + row * a.q_out_stride + h * DK;
-      store8<NT>(dst + c.c0, x);
-      store8<NT>(dst + c.c1, y);
+#pragma unroll
+      for (int i = 0; i < HEADS; ++i)
+        if (i < heads) {
+          store8<NT>(dst + i * DK + c.c0, x[i]);
+          store8<NT>(dst + i * DK + c.c1, y[i]);
+        }
       return;
     }
     const int64_t place = (((int64_t)page * kb.s.Hkv + h) << kb.page_shift) + ((int)p & (kb.pages.page_size - 1));
     TC* dst = is_value ? static_cast<TC*>(kb.pages.v) + place * DV : static_cast<TC*>(kb.pages.k) + place * DK;
-    if constexpr (kE4m3) {
-      const float scale = (is_value ? kb.pages.v_scale : kb.pages.k_scale)[h];
-      // The division is the IEEE one, so the stored bits are those of the formula.
+    const int64_t next_head = (int64_t)width << kb.page_shift;
 #pragma unroll
-      for (int n = 0; n < 8; ++n) x[n] = x[n] / scale, y[n] = y[n] / scale;
-      store8_e4m3<NT>(dst + c.c0, x);
-      store8_e4m3<NT>(dst + c.c1, y);
-    } else {
-      store8<NT>(dst + c.c0, x);
-      store8<NT>(dst + c.c1, y);
+    for (int i = 0; i < HEADS; ++i) {
+      if (i >= heads) continue;
+      if constexpr (kE4m3) {
+        const float scale = (is_value ? kb.pages.v_scale : kb.pages.k_scale)[h + i];
+        store8_e4m3<NT>(dst + i * next_head + c.c0, x[i], scale);
+        store8_e4m3<NT>(dst + i * next_head + c.c1, y[i], scale);
+      } else {
+        store8<NT>(dst + i * next_head + c.c0, x[i]);
+        store8<NT>(dst + i * next_head + c.c1, y[i]);
+      }
     }
   };
   if (live && b >= 0) append();
   return next;
 }
 
-template <int DK, int DV, typename TIn, typename TC, bool NT, bool AXES>
+template <int DK, int DV, typename TIn, typename TC, bool NT, bool AXES, int HEADS>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
   const KvBatch& kb = a.kb;
   // Ranges that do not fit the launch are named by the first block, whether
@@ -190,7 +206,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
   // turn computes is not kept for the next, which took 20 registers (8 prompts of
   // 8192 tokens to e4m3 364 us, now 285).
   for (int from = 0, begin = 0;;) {
-    from = append_unit<DK, DV, TIn, TC, NT, AXES>(a, here((int)(blockIdx.x * kThreads + threadIdx.x)), from, begin);
+    from = append_unit<DK, DV, TIn, TC, NT, AXES, HEADS>(
+        a, here((int)(blockIdx.x * kThreads + threadIdx.x)), from, begin);
     if (__ballot(from < kb.s.B) == 0) return;
     begin = from;
 #pragma unroll
@@ -204,29 +221,41 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
 // 303.  f32 and latent prompts lose by it (16384 f32 tokens 170 us for 147, 32768
 // latent ones 503 for 444).  What smaller calls write stays there for the
 // attention that reads it next.
-template <int DK, int DV, typename TIn, typename TC, bool AXES>
-hipError_t run(const AppendArgs& a, hipStream_t st) {
-  const int64_t units = (int64_t)a.kb.n_tokens * a.units, blocks = (units + kThreads - 1) / kThreads;
-  if (units * 16 * (int64_t)(sizeof(TIn) + sizeof(TC)) > (int64_t)256 << 20)
-    hipLaunchKernelGGL((append_kernel<DK, DV, TIn, TC, true, AXES>), dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
-  else
-    hipLaunchKernelGGL((append_kernel<DK, DV, TIn, TC, false, AXES>), dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
+template <int DK, int DV, typename TIn, typename TC, bool NT, bool AXES, int HEADS>
+hipError_t run(AppendArgs a, hipStream_t st) {
+  const kda_kv_shape& s = a.kb.s;
+  const auto groups = [](int32_t heads) { return (heads + HEADS - 1) / HEADS; };
+  a.units_q = a.q.p ? groups(s.Hq) * (DK / 16) : 0;
+  a.units_k = a.units_q + groups(s.Hkv) * (DK / 16);
+  a.units = a.units_k + (a.v.p ? groups(s.Hkv) * (DV / 16) : 0);
+  const int64_t blocks = ((int64_t)a.kb.n_tokens * a.units + kThreads - 1) / kThreads;
+  hipLaunchKernelGGL((append_kernel<DK, DV, TIn, TC, NT, AXES, HEADS>), dim3((unsigned)blocks), dim3(kThreads), 0, st,
+                     a);
   return hipGetLastError();
 }
 
+// Four heads to a thread (two of e4m3) where that leaves threads enough for the chip: 20000
+// tokens of 32 + 8 heads with pairs dealt to three axes 151 -> 104 us, but one
+// token 3.5 -> 4.8.
 template <int DK, int DV, typename TIn, typename TC>
 hipError_t run(const AppendArgs& a, hipStream_t st) {
-  return a.axes.n ? run<DK, DV, TIn, TC, true>(a, st) : run<DK, DV, TIn, TC, false>(a, st);
+  const kda_kv_shape& s = a.kb.s;
+  const int64_t values = a.kb.n_tokens * ((int64_t)s.Hkv * (DK + (a.v.p ? DV : 0)) + (a.q.p ? (int64_t)s.Hq * DK : 0));
+  const bool large = values * (int64_t)(sizeof(TIn) + sizeof(TC)) > (int64_t)256 << 20;
+  constexpr int kMost = sizeof(TC) == 1 ? 2 : 4;  // the divisions by a scale take registers
+  if (a.axes.n) {
+    if (large) return run<DK, DV, TIn, TC, true, true, kMost>(a, st);
+    if (values >= (int64_t)1 << 24) return run<DK, DV, TIn, TC, false, true, kMost>(a, st);
+    return run<DK, DV, TIn, TC, false, true, 1>(a, st);
+  }
+  return large ? run<DK, DV, TIn, TC, true, false, 1>(a, st) : run<DK, DV, TIn, TC, false, false, 1>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_kv_append(const KvBatch& b, KvRows k, KvRows v, KvRows q, void* q_out, int64_t q_out_stride,
                             const kda_rotation& rot, const Axes& axes, hipStream_t st) {
-  AppendArgs a{b, k, v, q, q_out, q_out_stride, rot, 0, 0, 0, axes};
-  a.units_q = q.p ? b.s.Hq * (b.s.dk / 16) : 0;
-  a.units_k = a.units_q + b.s.Hkv * (b.s.dk / 16);
-  a.units = a.units_k + (v.p ? b.s.Hkv * (b.s.dv / 16) : 0);
+  const AppendArgs a{b, k, v, q, q_out, q_out_stride, rot, 0, 0, 0, axes};
   if (b.s.dk == 576) return run<576, 512, bf16_t, bf16_t>(a, st);
   const bool wide = b.s.dk == 128;
   if (b.s.in_dtype == KDA_F32)

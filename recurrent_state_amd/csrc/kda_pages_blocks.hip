@@ -6,8 +6,7 @@
 // are only rotated), or for several where few tokens make few rows.  A group of
 // W waves holds 16 W rows of a head in registers, 16 values to a lane, laid out
 // as in kda_pages.hip; the maximum is exchanged by lane swaps and, for W > 1,
-// through the LDS.  Calls that bring more than 256 tokens to a block read them
-// twice.
+// through the LDS.
 //
 // The host knows neither lengths nor positions: the grid has an item for every
 // block that well-formed ranges can touch, each finds its sequence by a scan of
@@ -69,6 +68,7 @@ struct Item {
 __device__ __forceinline__ bool find_item(const BlocksArgs& a, int item, Item& it) {
   const int lane = threadIdx.x & 63, B = a.kb.s.B;
   int before = 0;
+#pragma unroll 1
   for (int c = 0; c < B; c += kWave) {
     const Places s = c + lane < B ? places_of(a, c + lane) : Places{};
     const int upto = wave_scan(s.blocks), sum = __builtin_amdgcn_readlane(upto, kWave - 1);
@@ -90,24 +90,27 @@ __device__ __forceinline__ bool find_item(const BlocksArgs& a, int item, Item& i
   return false;
 }
 
-// W waves to a (block, head); NW waves to a workgroup.
+// 16 values of a row of bf16 as loaded.
+struct Raw16 {
+  u32x4 lo, hi;
+};
+
+// W waves to a (block, kind); NW waves to a workgroup, which takes every
+// gridDim.y-th set of kinds of its item.  The angles of the item's rows stay in
+// registers, and the next kind's values are asked for before this one's are used.
 template <int D, int W, bool NT, bool AXES>
 __global__ void __launch_bounds__(64 * (W > 4 ? W : 4)) append_blocks_kernel(BlocksArgs a) {
-  constexpr int NW = W > 4 ? W : 4;
+  constexpr int NW = W > 4 ? W : 4, SETS = NW / W;
   constexpr int LPR = D / 16, RPP = kWave / LPR, PASSES = 16 / RPP;  // lanes to a row, rows of a wave's pass
-  __shared__ uint32_t lds_max[NW];
+  constexpr bool KEEP = W < 16 || D == 64;  // 1024 threads have no registers for angles and loads ahead
+  __shared__ uint32_t lds_max[2][NW];
   const KvBatch& kb = a.kb;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int part = wave % W, kind = blockIdx.y * (NW / W) + wave / W;
-  const bool is_key = kind < kb.s.Hkv, is_value = !is_key && kind < 2 * kb.s.Hkv;
-  const bool idle = kind >= a.kinds;
-  const int h = is_key ? kind : is_value ? kind - kb.s.Hkv : kind - 2 * kb.s.Hkv;
-  const int w = lane % LPR, n_rot = a.rot.cos_sin ? a.rot.dim >> 4 : 0;
-  const bool turn = !is_value && w < n_rot;
-  const Chunks c = is_value ? Chunks{16 * w, 16 * w + 8} : chunks_of(a.rot, n_rot, w);
-  const KvRows& rows = is_key ? a.k : is_value ? a.v : a.q;
-  const bf16_t* const src = static_cast<const bf16_t*>(rows.p) + h * D;
-  const bool names = blockIdx.y == 0 && wave < W;  // of the waves of an item's rows, those that name errors
+  const int part = wave % W, set = wave / W, w = lane % LPR;
+  const int n_rot = a.rot.cos_sin ? a.rot.dim >> 4 : 0;
+  const bool rotates = w < n_rot;
+  const Chunks c = chunks_of(a.rot, n_rot, w);
+  const bool names = blockIdx.y == 0 && set == 0;  // of the waves of an item's rows, those that name errors
 
   if (names && wave == 0 && blockIdx.x == 0)
     for (int b = lane; b < kb.s.B; b += kWave) {
@@ -118,108 +121,173 @@ __global__ void __launch_bounds__(64 * (W > 4 ? W : 4)) append_blocks_kernel(Blo
   Item it;
   for (int item = blockIdx.x; find_item(a, item, it); item += gridDim.x) {
     const int32_t page = kb.table[(int64_t)it.b * kb.max_pages + (it.begin >> kb.page_shift)];
-    const int chunks = W < 16 ? 1 : (it.hi - it.lo + 16 * W - 1) / (16 * W);  // see by_rows()
-    uint32_t m = 0;
-    float x[PASSES][8], y[PASSES][8];
+    // The lane's rows: token row, and place counted from the block's first.
+    int32_t row[PASSES], slot[PASSES];
     bool live[PASSES];
-    auto row_of = [&](int chunk, int pass) { return it.lo + (chunk * W + part) * 16 + pass * RPP + lane / LPR; };
-    auto load = [&](int chunk) __attribute__((always_inline)) {
+    float cc[KEEP ? PASSES : 1][8], ss[KEEP ? PASSES : 1][8];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const int p = it.lo + part * 16 + i * RPP + lane / LPR;
+      live[i] = p < it.hi;  // others stand for the first row, and are not stored
+      slot[i] = (live[i] ? p : it.lo) - it.begin;
+      row[i] = (int32_t)(it.row0 + (it.begin + slot[i] - it.pos));
+    }
+    auto fetch = [&](int kind, Raw16 (&x)[PASSES]) __attribute__((always_inline)) {
+      if (kind >= a.kinds) return;
+      const bool is_key = kind < kb.s.Hkv, is_value = !is_key && kind < 2 * kb.s.Hkv;
+      const int h = is_key ? kind : is_value ? kind - kb.s.Hkv : kind - 2 * kb.s.Hkv;
+      const void* const base = is_key ? a.k.p : is_value ? a.v.p : a.q.p;
+      const int64_t stride = is_key ? a.k.stride : is_value ? a.v.stride : a.q.stride;
+      const bf16_t* const src = static_cast<const bf16_t*>(base) + h * D;
 #pragma unroll
       for (int i = 0; i < PASSES; ++i) {
-        const int p = row_of(chunk, i);
-        live[i] = p < it.hi && !idle;
-        if (!live[i]) continue;
-        const int64_t row = it.row0 + (p - it.pos);
-        load8<NT>(src + row * rows.stride + c.c0, x[i]);
-        load8<NT>(src + row * rows.stride + c.c1, y[i]);
-        float cc[8], ss[8];
-        if constexpr (AXES) {
-          const AxisPos at = axis_positions(a.axes, a.rot, row);
-          if (at.bad) {
-            if (names && w == 0) set_err(kb.dev_err, KDA_DEV_ERR_POS);
-            live[i] = false;
-            continue;
-          }
-          if (turn) angles(a.rot, at, axes_of_unit<BlocksArgs>(w), w, cc, ss);
-        } else if (turn) {
-          angles(a.rot, p, w, cc, ss);
-        }
-        if (turn) rotate(x[i], y[i], cc, ss, a.rot.pairs);
+        const bf16_t* const at = src + here(row[i]) * stride;
+        x[i].lo = get<NT>(reinterpret_cast<const u32x4*>(at + c.c0));
+        x[i].hi = get<NT>(reinterpret_cast<const u32x4*>(at + c.c1));
       }
     };
-    const bool bad = page < 0 || page >= kb.pages.n_pages;
-    if (bad && names && lane == 0) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
-    if (bad) continue;  // the whole workgroup agrees
-    const bool stored = is_key || is_value;
-    const int64_t head = (int64_t)page * kb.s.Hkv + h;
-    float* const scale =
-        (is_key ? a.scales.k : a.scales.v) + (head << (kb.page_shift - a.scales.shift)) +
-        ((it.begin & (kb.pages.page_size - 1)) >> a.scales.shift);
-    uint8_t* const dst = static_cast<uint8_t*>(is_key ? kb.pages.k : kb.pages.v) +
-                         ((head << kb.page_shift) + (it.begin & (kb.pages.page_size - 1))) * D;
-    const bool joins = stored && !idle && it.lo > it.begin;
-    const float old = joins ? *scale : 0.f;
-    for (int chunk = 0; chunk < chunks && (stored || chunks == 1); ++chunk) {
-      load(chunk);
-#pragma unroll
-      for (int i = 0; i < PASSES; ++i)
-        if (live[i])
-#pragma unroll
-          for (int n = 0; n < 8; ++n) m = max(m, max(finite_bits(x[i][n]), finite_bits(y[i][n])));
-    }
-    m = wave_max(m);
-    if (W > 1) {
-      __syncthreads();  // the item before has been read
-      if (lane == 0) lds_max[wave] = m;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < W; ++i) m = max(m, lds_max[wave - part + i]);
-    }
-    uint32_t s = scale_for(m);
-    if (joins) {
-      s = max(s, power_of_two(old));
-      if (s != __float_as_uint(old)) {
-        const float f = old * inverse(s);
-        for (int r = part * RPP + lane / LPR; r < it.lo - it.begin; r += W * RPP) {
-          codes16* const at = reinterpret_cast<codes16*>(dst + r * D + 16 * w);
-          *at = rescaled(*at, f);
-        }
+    int kind = blockIdx.y * SETS + set;
+    Raw16 next[PASSES] = {};
+    if (KEEP) fetch(kind, next);
+    // Of a token that is skipped for its position, some angles.
+    auto turns = [&](int i, float (&c)[8], float (&s)[8]) __attribute__((always_inline)) {
+      if constexpr (AXES) {
+        AxisPos at = axis_positions(a.axes, a.rot, here(row[i]));
+        if (at.bad) at.p0 = at.p1 = at.p2 = at.p3 = 0;
+        angles(a.rot, at, axes_of_unit<BlocksArgs>(w), w, c, s);
+      } else {
+        angles(a.rot, it.begin + here(slot[i]), w, c, s);
       }
+    };
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      if (AXES && axis_positions(a.axes, a.rot, row[i]).bad) {
+        if (names && w == 0) set_err(kb.dev_err, KDA_DEV_ERR_POS);
+        live[i] = false;
+      }
+      if (KEEP && rotates) turns(i, cc[i], ss[i]);
     }
-    const float inv = inverse(s);
-    if (stored && !idle && part == 0 && lane == 0) *scale = __uint_as_float(s);
-    for (int chunk = 0; chunk < chunks; ++chunk) {
-      if (chunks > 1) load(chunk);
+    const bool bad = page < 0 || page >= kb.pages.n_pages;
+    if (bad && names && wave == 0 && lane == 0) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
+    if (bad) continue;  // the whole workgroup agrees
+    const int in_page = it.begin & (kb.pages.page_size - 1);
+
+#pragma unroll 1
+    for (int turn = 0; kind - set < a.kinds; ++turn, kind += gridDim.y * SETS) {
+      const bool is_key = kind < kb.s.Hkv, is_value = !is_key && kind < 2 * kb.s.Hkv;
+      const int h = is_key ? kind : is_value ? kind - kb.s.Hkv : kind - 2 * kb.s.Hkv;
+      const bool stored = is_key || is_value;
+      const int64_t head = (int64_t)page * kb.s.Hkv + h;
+      float* const scale = (is_key ? a.scales.k : a.scales.v) + (head << (kb.page_shift - a.scales.shift)) +
+                           (in_page >> a.scales.shift);
+      uint8_t* const dst =
+          static_cast<uint8_t*>(is_key ? kb.pages.k : kb.pages.v) + ((head << kb.page_shift) + in_page) * D;
+      const bool joins = stored && it.lo > it.begin;
+      const float old = joins ? *scale : 0.f;
+      Raw16 now[PASSES];
+      if (!KEEP) fetch(kind, next);
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) now[i] = next[i];
+      if (KEEP) fetch(kind + gridDim.y * SETS, next);
+      // The lane's values of pass i, rotated: made twice, for the maximum and to
+      // be stored, as keeping them takes twice the registers.
+      float x[8], y[8];
+      auto make = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t lo = here(now[i].lo[n]), hi = here(now[i].hi[n]);
+          x[2 * n] = bf16_lo(lo), x[2 * n + 1] = bf16_hi(lo);
+          y[2 * n] = bf16_lo(hi), y[2 * n + 1] = bf16_hi(hi);
+        }
+        if (rotates && !is_value) {
+          if constexpr (!KEEP) turns(i, cc[0], ss[0]);
+          rotate(x, y, cc[KEEP ? i : 0], ss[KEEP ? i : 0], a.rot.pairs);
+        }
+      };
+      uint32_t s = 0;
+      bool odd = false;  // some value of the lane's is not finite
+      // Sets of one workgroup may be at keys, values and queries: those of the
+      // first one come first.
+      if (kind - set < 2 * kb.s.Hkv) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+          uint32_t top = 0;
+          make(i);
+#pragma unroll
+          for (int n = 0; n < 8; ++n) top = max(top, max(magnitude(x[n]), magnitude(y[n])));
+          if (top > kLargest) {
+            odd = true;
+            top = 0;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) top = max(top, max(finite_bits(x[n]), finite_bits(y[n])));
+          }
+          m = max(m, live[i] ? top : 0);
+        }
+        m = wave_max(m);
+        if (W > 1) {
+          if (lane == 0) lds_max[turn & 1][wave] = m;
+          __syncthreads();
+#pragma unroll
+          for (int i = 0; i < W; ++i) m = max(m, lds_max[turn & 1][wave - part + i]);
+        }
+        s = scale_for(m);
+        if (joins) {
+          s = max(s, power_of_two(old));
+          if (s != __float_as_uint(old)) {
+            const float f = old * inverse(s);
+#pragma unroll 1
+            for (int r = part * RPP + lane / LPR; r < it.lo - it.begin; r += W * RPP) {
+              codes16* const at = reinterpret_cast<codes16*>(dst + r * D + 16 * w);
+              *at = rescaled(*at, f);
+            }
+          }
+        }
+        if (stored && part == 0 && lane == 0) *scale = __uint_as_float(s);
+      }
 #pragma unroll
       for (int i = 0; i < PASSES; ++i) {
-        if (!live[i]) continue;
-        const int p = row_of(chunk, i);
+        make(i);
         if (stored) {
+          const float inv = inverse(s);
 #pragma unroll
-          for (int n = 0; n < 8; ++n) x[i][n] *= inv, y[i][n] *= inv;
-          uint8_t* const to = dst + (p - it.begin) * D;
-          store8_e4m3<NT>(to + c.c0, x[i]);
-          store8_e4m3<NT>(to + c.c1, y[i]);
-        } else {
-          bf16_t* const to = static_cast<bf16_t*>(a.q_out) + (it.row0 + (p - it.pos)) * a.q_out_stride + h * D;
-          store8<NT>(to + c.c0, x[i]);
-          store8<NT>(to + c.c1, y[i]);
+          for (int n = 0; n < 8; ++n) x[n] *= inv, y[n] *= inv;
+          if (odd) {  // the others are at most 448
+#pragma unroll
+            for (int n = 0; n < 8; ++n) x[n] = to_range(x[n]), y[n] = to_range(y[n]);
+          }
+          uint8_t* const to = dst + here(slot[i]) * D;
+          if (live[i]) {
+            put<NT>(reinterpret_cast<u32x2*>(to + c.c0), e4m3_of(x));
+            put<NT>(reinterpret_cast<u32x2*>(to + c.c1), e4m3_of(y));
+          }
+        } else if (kind < a.kinds) {
+          bf16_t* const to = static_cast<bf16_t*>(a.q_out) + here(row[i]) * a.q_out_stride + h * D;
+          if (live[i]) {
+            store8<NT>(to + c.c0, x);
+            store8<NT>(to + c.c1, y);
+          }
         }
       }
     }
+    if (W > 1) __syncthreads();  // the last maxima have been read
   }
 }
 
 template <int D, int W, bool NT>
 hipError_t run(const BlocksArgs& a, hipStream_t st) {
-  constexpr int NW = W > 4 ? W : 4;
+  constexpr int NW = W > 4 ? W : 4, SETS = NW / W;
   const int64_t N = a.kb.n_tokens, B = a.kb.s.B;
   int64_t items = (N >> a.scales.shift) + 2 * B;
   if (items > N) items = N;
-  const unsigned y = (a.kinds + NW / W - 1) / (NW / W);
-  const int64_t most = (((int64_t)1 << 32) - 1) / ((int64_t)y * NW * kWave);  // threads of a launch
+  // Workgroups to an item: as many as it has sets of kinds, or fewer where the
+  // items alone make 2048 workgroups.
+  const int64_t sets = (a.kinds + SETS - 1) / SETS;
+  int64_t y = 2048 / items;
+  y = y < 1 ? 1 : y > sets ? sets : y;
+  const int64_t most = (((int64_t)1 << 32) - 1) / (y * NW * kWave);  // threads of a launch
   if (items > most) items = most;
-  const dim3 grid((unsigned)items, y), block(NW * kWave);
+  const dim3 grid((unsigned)items, (unsigned)y), block(NW * kWave);
   if (a.axes.n)
     hipLaunchKernelGGL((append_blocks_kernel<D, W, NT, true>), grid, block, 0, st, a);
   else
@@ -229,7 +297,7 @@ hipError_t run(const BlocksArgs& a, hipStream_t st) {
 
 template <int D, bool NT>
 hipError_t by_rows(const BlocksArgs& a, hipStream_t st) {
-  // Waves enough for the rows that a call can bring to a block, up to 16.
+  // Waves enough for the rows that a call can bring to a block.
   const int block = 1 << a.scales.shift, rows = a.kb.s.T < block ? a.kb.s.T : block;
   if (rows <= 16) return run<D, 1, NT>(a, st);
   if (rows <= 32) return run<D, 2, NT>(a, st);
