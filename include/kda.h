@@ -738,8 +738,9 @@ kda_status kda_attn_decode_blocks(const kda_kv_shape* shape, const kda_pages* pa
  *            max_pages * page_size
  * Grouped form; scales NULL: pages as kda_attn_decode, else as
  * kda_attn_decode_blocks.  1 <= T <= 128 (a decode token, drafts, or the last
- * tokens of a prompt); otherwise limits as kda_attn_decode.  Every sum is made
- * in one order: equal calls give equal bits.  Sequences are refused as by
+ * tokens of a prompt), B * max_pages * page_size at most about 2^34 tokens;
+ * otherwise limits as kda_attn_decode.  Every sum is made in one order: equal
+ * calls give equal bits.  Sequences are refused as by
  * kda_attn_decode, except that a page id outside [0, n_pages) (KDA_DEV_ERR_PAGE)
  * costs the tokens of that page only.
  */

@@ -144,8 +144,8 @@ kda_status check_kv_shape(const kda_kv_shape* s, const kda_pages* pages, int32_t
 
 // kda_attn_decode counts the tiles (32 tokens or more) of all sequences in 32
 // bits, and its join has a block of up to 1024 threads to each sequence.
-bool tiles_fit(const kda_kv_shape& s, int32_t page_size, int32_t max_pages) {
-  return s.B <= 1 << 20 && (int64_t)s.B * ((int64_t)max_pages * page_size / 32 + 2) <= (int64_t)1 << 30;
+bool tiles_fit(const kda_kv_shape& s, int32_t page_size, int32_t max_pages, int tile = 32) {
+  return s.B <= 1 << 20 && (int64_t)s.B * ((int64_t)max_pages * page_size / tile + 2) <= (int64_t)1 << 30;
 }
 bool attends(const kda_kv_shape& s, int32_t page_size, int32_t max_pages) {
   return s.T <= kMaxT && tiles_fit(s, page_size, max_pages);
@@ -837,7 +837,7 @@ kda_status kda_attn_weights(const kda_kv_shape* shape, const kda_pages* pages, c
   kda_status r = check_kv(shape, pages, table, max_pages, tok_start, n_tokens, pos, dev_err, &b, !scales);
   if (r != KDA_OK) return r;
   const kda_kv_shape& s = *shape;
-  if (is_latent(s) || s.T > kMaxWeighed || !tiles_fit(s, pages->page_size, max_pages)) return KDA_ERR_SHAPE;
+  if (is_latent(s) || s.T > kMaxWeighed || !tiles_fit(s, pages->page_size, max_pages, 16)) return KDA_ERR_SHAPE;
   if (window < 0 || !isfinite(scale)) return KDA_ERR_SHAPE;
   const bool empty = s.B == 0 || n_tokens == 0;
   kda::BlockScales bs{};

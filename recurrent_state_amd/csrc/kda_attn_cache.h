@@ -109,12 +109,23 @@ struct Cache<D, bf16_t, NT> {
     for (int s = 0; s < D / 32; ++s) c = mfma_bf16(__builtin_bit_cast(bf16x8, k[u][s]), q.q[s], c);
     return c;
   }
-  // S = Q K^T: a token to each lane column, query rows 4 (l >> 4) + i.
-  __device__ __forceinline__ f32x4 score_t(int u, const Query& q) const {
-    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+  // The keys as operands, and S = Q K^T from them, contraction step by step: a
+  // token to each lane column, query rows 4 (l >> 4) + i.
+  struct Keys {
+    static constexpr int STEPS = D / 32;
+    bf16x8 k[2][STEPS];
+
+    __device__ __forceinline__ void add(int u, int s, const Query& q, f32x4& c) const {
+      c = mfma_bf16(q.q[s], k[u][s], c);
+    }
+  };
+  __device__ __forceinline__ Keys keys() const {
+    Keys x;
 #pragma unroll
-    for (int s = 0; s < D / 32; ++s) c = mfma_bf16(q.q[s], __builtin_bit_cast(bf16x8, k[u][s]), c);
-    return c;
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s) x.k[u][s] = __builtin_bit_cast(bf16x8, k[u][s]);
+    return x;
   }
   // Values of the lane's token e (of 8: group e >> 2): zero unless kept / tested.
   __device__ __forceinline__ void keep(int e, bool kept) {
@@ -155,9 +166,7 @@ struct Cache<D, uint8_t, NT> {
   static constexpr int VC = D / 16;
   u32x4 k[2][D / 64];
   uint32_t v[8][VC / 4];
-  struct Query {
-    bf16x8 q[D / 32];
-  };
+  typedef typename Cache<D, bf16_t, NT>::Query Query;
 
   static __device__ __forceinline__ void load_query(Query& q, const bf16_t* row, bool live) {
     const int g = (threadIdx.x & 63) >> 4;
@@ -195,15 +204,17 @@ struct Cache<D, uint8_t, NT> {
     }
     return c;
   }
-  __device__ __forceinline__ f32x4 score_t(int u, const Query& q) const {
-    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+  typedef typename Cache<D, bf16_t, NT>::Keys Keys;  // takes a Query of this layout too
+  __device__ __forceinline__ Keys keys() const {
+    Keys x;
 #pragma unroll
-    for (int s = 0; s < D / 32; ++s) {
-      const uint32_t a = k[u][s / 2][2 * (s & 1)], b = k[u][s / 2][2 * (s & 1) + 1];
-      c = mfma_bf16(q.q[s], as_op(widen_e4m3<false>(a), widen_e4m3<true>(a), widen_e4m3<false>(b), widen_e4m3<true>(b)),
-                    c);
-    }
-    return c;
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s) {
+        const uint32_t a = k[u][s / 2][2 * (s & 1)], b = k[u][s / 2][2 * (s & 1) + 1];
+        x.k[u][s] = as_op(widen_e4m3<false>(a), widen_e4m3<true>(a), widen_e4m3<false>(b), widen_e4m3<true>(b));
+      }
+    return x;
   }
   __device__ __forceinline__ void keep(int e, bool kept) {
 #pragma unroll
@@ -270,13 +281,19 @@ struct Cache<D, float, NT> {
       for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(k[u][s][i], q.q[s][i], c, 0, 0, 0);
     return c;
   }
-  __device__ __forceinline__ f32x4 score_t(int u, const Query& q) const {
-    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+  struct Keys {
+    static constexpr int STEPS = D / 4;
+    f32x4 k[1][D / 16];
+
+    __device__ __forceinline__ void add(int u, int s, const Query& q, f32x4& c) const {
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(q.q[s >> 2][s & 3], k[u][s >> 2][s & 3], c, 0, 0, 0);
+    }
+  };
+  __device__ __forceinline__ Keys keys() const {
+    Keys x;
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(q.q[s][i], k[u][s][i], c, 0, 0, 0);
-    return c;
+    for (int s = 0; s < D / 16; ++s) x.k[0][s] = k[0][s];
+    return x;
   }
   __device__ __forceinline__ void keep(int e, bool kept) {
 #pragma unroll
