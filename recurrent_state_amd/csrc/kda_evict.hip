@@ -1,16 +1,20 @@
 // Eviction from the paged cache: which tokens each kv head keeps, and their move
 // to other pages.
 //
-//   select  One workgroup to a (sequence, kv head).  The keys that order the
-//           candidates are 32-bit numbers; the k-th greatest is found digit by
-//           digit (11, 11 and 10 bits), each a histogram in the LDS of those that
-//           share the digits above.  Then every wave counts, in its own stretch
-//           of tokens, those above it and those equal to it, and after one scan
-//           over the waves writes its kept places in order.
+//   select  One workgroup to a (sequence, kv head), or, for few long rows, one to
+//           every 8192 of its tokens.  The keys that order the candidates are
+//           32-bit numbers; the k-th greatest is found digit by digit (11, 11 and
+//           10 bits), each a histogram in the LDS of those that share the digits
+//           above.  Then every wave counts, in its own stretch of tokens, those
+//           above it and those equal to it, and after one scan over the waves
+//           writes its kept places in order.  Bound by the passes' latency:
+//           8 heads' 100001 tokens take 27 us in parts, 64 by one workgroup each;
+//           64 sequences of up to 8191 tokens, 8 heads, 15 us.
 //   move    Rows go from their places to the new ones.  Pages without scales or
 //           with scales by heads are copied 16 bytes to a thread; where scales go
 //           by blocks, a group of waves takes a new block, whose scale is that of
-//           its largest value.
+//           its largest value.  Bound by memory: 20000 tokens of 8 heads of 128 in
+//           bf16 32 us (5.2 TB/s), those 64 sequences cut to 2000 e4m3 tokens 60.
 
 #include "kda_blocks.h"
 
@@ -83,12 +87,33 @@ __device__ __forceinline__ void clear_hist(SelectLds& lds) {
   __syncthreads();
 }
 
-// The k greatest of n weights, 0 < k < n: their places to kept, in order, and the
-// weights to out_w.  A wave has a stretch of neighbours, 64 at a time.  V: a
-// thread's share, held in registers; 0: more than that, read again for every
-// pass, kBatch at once.
+// The places that a wave keeps: behind those of the waves before it (lds.gt and
+// lds.eq, which all have set) and gt and eq of the parts before those.
+struct Kept {
+  uint32_t gt, eq;  // so far: above the threshold, and at it
+
+  __device__ __forceinline__ Kept(const SelectLds& lds, uint32_t gt0, uint32_t eq0) : gt(gt0), eq(eq0) {
+    const int wave = threadIdx.x >> 6;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSelectWaves; ++i) gt += i < wave ? lds.gt[i] : 0, eq += i < wave ? lds.eq[i] : 0;
+    gt = __builtin_amdgcn_readfirstlane(gt), eq = __builtin_amdgcn_readfirstlane(eq);
+  }
+  // Of those at the threshold `top` the first `equal` are kept.
+  __device__ __forceinline__ void put(int32_t* kept, int j, uint32_t key, bool there, uint32_t top, uint32_t equal) {
+    const uint64_t is_gt = __ballot(there && key > top), is_eq = __ballot(there && key == top);
+    const uint32_t e = lanes_before(is_eq, eq);
+    if (there && (key > top || (key == top && e < equal))) kept[lanes_before(is_gt, gt) + min(e, equal)] = j;
+    gt += __popcll(is_gt);
+    eq += __popcll(is_eq);
+  }
+};
+
+// The k greatest of n weights, 0 < k < n: their places to kept, in order.  A wave
+// has a stretch of neighbours, 64 at a time.  V: a thread's share, held in
+// registers; 0: more than that, read again for every pass, kBatch at once.
 template <int V>
-__device__ __forceinline__ void select(const float* w, int n, int k, int32_t* kept, float* out_w, SelectLds& lds) {
+__device__ __forceinline__ void select(const float* w, int n, int k, int32_t* kept, SelectLds& lds) {
   constexpr int kBatch = 16;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int each = V > 0 ? V * kWave : (n + kSelect * kBatch - 1) / (kSelect * kBatch) * (kWave * kBatch);
@@ -195,68 +220,191 @@ __device__ __forceinline__ void select(const float* w, int n, int k, int32_t* ke
     if (lane == 0) lds.gt[wave] = gt, lds.eq[wave] = eq;
   }
   __syncthreads();
-  uint32_t gt = 0, eq = 0;
-#pragma unroll
-  for (int i = 0; i < kSelectWaves; ++i) gt += i < wave ? lds.gt[i] : 0, eq += i < wave ? lds.eq[i] : 0;
-  gt = __builtin_amdgcn_readfirstlane(gt), eq = __builtin_amdgcn_readfirstlane(eq);
-  all([&](int j, float x, bool there) {
-    const uint32_t key = order(x);
-    const uint64_t is_gt = __ballot(there && key > top), is_eq = __ballot(there && key == top);
-    const uint32_t e = lanes_before(is_eq, eq);
-    if (there && (key > top || (key == top && e < equal))) {
-      const uint32_t at = lanes_before(is_gt, gt) + min(e, equal);
-      kept[at] = j;
-      out_w[at] = x;
-    }
-    gt += __popcll(is_gt);
-    eq += __popcll(is_eq);
-  });
+  Kept from(lds, 0, 0);
+  all([&](int j, float x, bool there) { from.put(kept, j, order(x), there, top, equal); });
 }
+
+// What is done with a (sequence, kv head).
+struct Row {
+  const float* w;
+  float* out_w;
+  int32_t* kept;
+  int L, n, k;  // length, candidates, how many of them are kept
+  bool bad, stays;
+
+  __device__ __forceinline__ Row(const EvictArgs& a, int64_t bh) {
+    const int64_t len = a.kb.pos[bh / a.kb.s.Hkv];
+    w = a.weights + bh * a.stride;
+    out_w = a.new_weights + bh * a.stride;
+    kept = a.kept + bh * a.keep;
+    bad = len < 0 || len > ((int64_t)a.kb.max_pages << a.kb.page_shift);
+    L = bad ? 0 : (int)len;
+    stays = L <= a.keep;
+    n = L - a.recent;
+    k = a.keep - a.recent;
+  }
+  // Whether the pages of a sequence to be cut are all there; by a whole workgroup.
+  __device__ __forceinline__ void check_pages(const EvictArgs& a, int b) {
+    const KvBatch& kb = a.kb;
+    if (bad || stays) return;
+    const auto outside = [&](int32_t id) { return id < 0 || id >= kb.pages.n_pages; };
+    const int last = kb.pages.page_size - 1;
+    bool off = false;
+    for (int i = threadIdx.x; i < (L + last) >> kb.page_shift; i += kSelect)
+      off |= outside(kb.table[(int64_t)b * kb.max_pages + i]);
+    for (int i = threadIdx.x; i < (a.keep + last) >> kb.page_shift; i += kSelect)
+      off |= outside(a.dst_table[(int64_t)b * a.dst_max_pages + i]);
+    bad = __syncthreads_or(off);
+  }
+  // Part `part` of `parts` of the results that no choice enters: of a row that is
+  // left alone all of them, of another the last tokens.
+  __device__ __forceinline__ void plain(const EvictArgs& a, int part, int parts) const {
+    const int tid = part * kSelect + threadIdx.x, step = parts * kSelect;
+    if (bad || stays) {
+      for (int i = tid; i < a.keep; i += step) kept[i] = -1;
+      for (int64_t j = tid; j < a.stride; j += step) out_w[j] = !bad && j < L ? w[j] : 0.f;
+    } else {
+      for (int i = tid; i < a.recent; i += step) kept[k + i] = n + i;
+    }
+  }
+};
 
 // LONG: rows may have more than kShort candidates.
 template <bool LONG>
 __global__ void __launch_bounds__(kSelect, LONG ? 4 : 8) select_kernel(EvictArgs a) {
   __shared__ SelectLds lds;
-  const KvBatch& kb = a.kb;
-  const int tid = threadIdx.x;
-  const int b = blockIdx.x / kb.s.Hkv;
-  const float* const w = a.weights + (int64_t)blockIdx.x * a.stride;
-  float* const out_w = a.new_weights + (int64_t)blockIdx.x * a.stride;
-  int32_t* const kept = a.kept + (int64_t)blockIdx.x * a.keep;
-  const int64_t len = kb.pos[b];
-  bool bad = len < 0 || len > ((int64_t)kb.max_pages << kb.page_shift);
-  const int L = bad ? 0 : (int)len;
-  const bool stays = L <= a.keep;
-  if (!bad && !stays) {
-    const int page_size = kb.pages.page_size;
-    const auto outside = [&](int32_t id) { return id < 0 || id >= kb.pages.n_pages; };
-    bool off = false;
-    for (int i = tid; i < (L + page_size - 1) >> kb.page_shift; i += kSelect)
-      off |= outside(kb.table[(int64_t)b * kb.max_pages + i]);
-    for (int i = tid; i < (a.keep + page_size - 1) >> kb.page_shift; i += kSelect)
-      off |= outside(a.dst_table[(int64_t)b * a.dst_max_pages + i]);
-    bad = __syncthreads_or(off);
-  }
-  if (bad && tid == 0) set_err(kb.dev_err, KDA_DEV_ERR_PAGE);
-  if (bad || stays) {
-    for (int i = tid; i < a.keep; i += kSelect) kept[i] = -1;
-    for (int64_t j = tid; j < a.stride; j += kSelect) out_w[j] = !bad && j < L ? w[j] : 0.f;
-    return;
-  }
+  Row r(a, blockIdx.x);
+  r.check_pages(a, blockIdx.x / a.kb.s.Hkv);
+  if (r.bad && threadIdx.x == 0) set_err(a.kb.dev_err, KDA_DEV_ERR_PAGE);
+  r.plain(a, 0, 1);
+  if (r.bad || r.stays || r.k == 0) return;
+  if (!LONG || r.n <= kShort)
+    select<kShort / kSelect>(r.w, r.n, r.k, r.kept, lds);
+  else
+    select<0>(r.w, r.n, r.k, r.kept, lds);
+}
 
-  // The n candidates, of which the k greatest are kept.
-  const int n = L - a.recent, k = a.keep - a.recent;
-  if (k > 0) {
-    if (!LONG || n <= kShort)
-      select<kShort / kSelect>(w, n, k, kept, out_w, lds);
-    else
-      select<0>(w, n, k, kept, out_w, lds);
+// The same with a row's candidates shared out to workgroups, kShort to each, for
+// few long rows: a launch for each digit's histogram, by parts, and one that adds
+// up the last one's and writes the places.  The row's new_weights, which the move
+// writes after them, hold the histograms meanwhile.
+struct Parts {
+  uint32_t* hist[3];  // [part][bins of the digit]
+  uint32_t* gt;       // [part]: keys above the first two digits
+  uint32_t* row;      // first digit, keys above it, first two digits, keys above them
+
+  static constexpr int kBinsOf[3] = {2048, 2048, 1024};
+  __device__ __forceinline__ Parts(const Row& r, int parts) {
+    hist[0] = reinterpret_cast<uint32_t*>(r.out_w);
+    hist[1] = hist[0] + parts * 2048;
+    hist[2] = hist[1] + parts * 2048;
+    gt = hist[2] + parts * 1024;
+    row = gt + parts;
   }
-  for (int i = tid; i < a.recent; i += kSelect) {
-    kept[k + i] = n + i;
-    out_w[k + i] = w[n + i];
+  // Words of a row that this takes; no more than a row of (parts - 1) kShort has, from three parts on.
+  static constexpr int64_t words(int64_t parts) { return parts * (2048 + 2048 + 1024 + 1) + 4; }
+
+  // The sum of a digit's histograms of the row's parts to lds.hist.
+  __device__ __forceinline__ void add_up(int digit, int count, SelectLds& lds) const {
+    uint32_t c[2] = {0, 0};
+    const uint32_t* p = hist[digit] + threadIdx.x;
+#pragma unroll 8
+    for (int i = 0; i < count; ++i) {
+      c[0] += p[i * kBinsOf[digit]];
+      if (digit < 2) c[1] += p[i * kBinsOf[digit] + kSelect];
+    }
+    lds.hist[threadIdx.x] = c[0], lds.hist[threadIdx.x + kSelect] = c[1];
   }
-  for (int64_t j = a.keep + tid; j < a.stride; j += kSelect) out_w[j] = 0.f;
+};
+
+// Rows are shared out where one workgroup to a row leaves most of the chip idle
+// and takes longer than four launches.  Whole calls, shared out and not: 8 rows of
+// 41000 tokens 28 and 28 us, of 57000 30 and 35, of 180000 40 and 70; 32 rows 38 and
+// 37, 40 and 45, 80 and 82; 64 rows of 57000 57 and 52, of 120000 95 and 72.
+constexpr int kFewestParts = 6, kMostRows = 32, kMostParts = 1024;
+constexpr int kEach = kShort / kSelect;  // of a thread: every 64th of its wave's stretch
+
+struct Stretch {
+  int j0;
+  uint32_t key[kEach];
+
+  __device__ __forceinline__ Stretch(const Row& r, int part) : j0(part * kShort + (threadIdx.x >> 6) * (kEach * kWave)) {
+    float x[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) x[i] = there(r, i) ? r.w[place(i)] : 0.f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) key[i] = order(x[i]);
+  }
+  __device__ __forceinline__ int place(int i) const { return j0 + i * kWave + (threadIdx.x & 63); }
+  __device__ __forceinline__ bool there(const Row& r, int i) const { return place(i) < r.n; }
+};
+
+template <int DIGIT>
+__global__ void __launch_bounds__(kSelect) hist_kernel(EvictArgs a, int parts) {
+  __shared__ SelectLds lds;
+  const int part = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+  const Row r(a, blockIdx.x);
+  if (r.bad || r.stays || r.k == 0 || part * kShort >= r.n) return;
+  const Parts p(r, parts);
+  const Stretch mine(r, part);
+  uint32_t top = 0;
+  if (DIGIT > 0) {
+    p.add_up(DIGIT - 1, (r.n + kShort - 1) / kShort, lds);
+    find_digit(lds, DIGIT == 1 ? 0 : p.row[1], r.k);
+    top = DIGIT == 1 ? lds.found[0] : p.row[0] << 11 | lds.found[0];
+    if (part == 0 && tid == 0) p.row[2 * DIGIT - 2] = top, p.row[2 * DIGIT - 1] = lds.found[1];
+  }
+  if (tid == 0) lds.length = 0;
+  clear_hist(lds);
+  constexpr int kShift[3] = {21, 10, 0};
+  uint32_t gt = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const uint32_t key = mine.key[i], digits = key >> kShift[DIGIT];
+    const bool there = mine.there(r, i);
+    const uint32_t before = DIGIT == 0 ? 0 : DIGIT == 1 ? key >> 21 : key >> 10;
+    if (DIGIT == 2) gt += __popcll(__ballot(there && before > top));
+    if (there && (DIGIT == 0 || before == top)) atomicAdd(&lds.hist[digits & (Parts::kBinsOf[DIGIT] - 1)], 1u);
+  }
+  if (DIGIT == 2 && lane == 0) atomicAdd(&lds.length, gt);
+  __syncthreads();
+  for (int i = tid; i < Parts::kBinsOf[DIGIT]; i += kSelect) p.hist[DIGIT][part * Parts::kBinsOf[DIGIT] + i] = lds.hist[i];
+  if (DIGIT == 2 && tid == 0) p.gt[part] = lds.length;
+}
+
+__global__ void __launch_bounds__(kSelect) places_kernel(EvictArgs a, int parts) {
+  __shared__ SelectLds lds;
+  const int part = blockIdx.y, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  Row r(a, blockIdx.x);
+  r.check_pages(a, blockIdx.x / a.kb.s.Hkv);
+  if (r.bad && part == 0 && tid == 0) set_err(a.kb.dev_err, KDA_DEV_ERR_PAGE);
+  r.plain(a, part, parts);
+  if (r.bad || r.stays || r.k == 0 || part * kShort >= r.n) return;
+  const Parts p(r, parts);
+  const Stretch mine(r, part);
+  p.add_up(2, (r.n + kShort - 1) / kShort, lds);
+  find_digit(lds, p.row[3], r.k);
+  const uint32_t digit = lds.found[0], top = p.row[2] << 10 | digit, equal = (uint32_t)r.k - lds.found[1];
+  // Kept ones of the parts before this, then of the waves.
+  __syncthreads();
+  if (tid == 0) lds.found[0] = lds.found[1] = 0;
+  __syncthreads();
+  uint32_t gt = tid < part ? p.gt[tid] : 0, eq = tid < part ? p.hist[2][tid * 1024 + digit] : 0;
+  if ((uint32_t)tid > digit)
+    for (int i = 0; i < part; ++i) gt += p.hist[2][i * 1024 + tid];
+  if (gt) atomicAdd(&lds.found[0], gt);
+  if (eq) atomicAdd(&lds.found[1], eq);
+  gt = eq = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    gt += __popcll(__ballot(mine.there(r, i) && mine.key[i] > top));
+    eq += __popcll(__ballot(mine.there(r, i) && mine.key[i] == top));
+  }
+  if (lane == 0) lds.gt[wave] = gt, lds.eq[wave] = eq;
+  __syncthreads();
+  Kept from(lds, lds.found[0], lds.found[1]);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) from.put(r.kept, mine.place(i), mine.key[i], mine.there(r, i), top, equal);
 }
 
 // Where a place of a sequence lies, in rows of the pool.
@@ -269,34 +417,47 @@ __device__ __forceinline__ void set_length(const EvictArgs& a, int b) {
   if (threadIdx.x == 0) a.new_len[b] = a.kept[(int64_t)b * a.kb.s.Hkv * a.keep] >= 0 ? a.keep : a.kb.pos[b];
 }
 
-constexpr int kMove = 256;
+// The weights of the kept tokens, and zeros behind them: a workgroup's share.
+__device__ __forceinline__ void move_weights(const EvictArgs& a, int64_t bh, const int32_t* kept, int part, int parts) {
+  const float* const w = a.weights + bh * a.stride;
+  float* const out = a.new_weights + bh * a.stride;
+  for (int64_t j = (int64_t)part * blockDim.x + threadIdx.x; j < a.stride; j += (int64_t)parts * blockDim.x)
+    out[j] = j < a.keep ? w[kept[j]] : 0.f;
+}
 
-// Rows of `units` 16-byte units, keys and values together.  Workgroups (b, part) by x; kv heads by y.
+// kAtOnce: loads on their way of a thread (2 and 8 took as long).
+constexpr int kMove = 256, kAtOnce = 4;
+
+// Rows of `units` 16-byte units, keys and values together.  Workgroups (b, part) by
+// x; kv heads by y.  The tokens' old places are read for the last time, so past the
+// caches (100001 tokens to 20000, 8 heads of 128 in bf16: 33 us for 40).
 template <bool VALUES>
 __global__ void __launch_bounds__(kMove) move_kernel(EvictArgs a, int units, int parts) {
-  constexpr int kAtOnce = 4;
   const KvBatch& kb = a.kb;
   const int b = blockIdx.x / parts, part = blockIdx.x % parts, h = blockIdx.y;
   if (part == 0 && h == 0) set_length(a, b);
   const int32_t* const kept = a.kept + ((int64_t)b * kb.s.Hkv + h) * a.keep;
   if (kept[0] < 0) return;
+  move_weights(a, (int64_t)b * kb.s.Hkv + h, kept, part, parts);
   u32x4* const k = static_cast<u32x4*>(kb.pages.k);
   u32x4* const v = static_cast<u32x4*>(kb.pages.v);
   const int32_t* const from = kb.table + (int64_t)b * kb.max_pages;
   const int32_t* const to = a.dst_table + (int64_t)b * a.dst_max_pages;
   const int64_t total = (int64_t)a.keep * units;
-  for (int64_t x0 = (int64_t)part * (kMove * kAtOnce) + threadIdx.x; x0 < total; x0 += (int64_t)parts * (kMove * kAtOnce)) {
+  const uint32_t by = (1u << 20) / units + 1;  // x / units = x * by >> 20 for x < 2^11, units up to 2^9
+  for (int64_t x0 = (int64_t)part * (kMove * kAtOnce); x0 < total; x0 += (int64_t)parts * (kMove * kAtOnce)) {
+    const int i0 = (int)(x0 / units), c0 = (int)(x0 - (int64_t)i0 * units);
     u32x4 xk[kAtOnce], xv[kAtOnce];
     int64_t dst[kAtOnce];
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
-      const int64_t x = x0 + u * kMove;
+      const uint32_t x = c0 + u * kMove + threadIdx.x, row = x * by >> 20, c = x - row * units;
+      const int i = i0 + (int)row;
       dst[u] = -1;
-      if (x >= total) continue;
-      const int i = (int)(x / units), c = (int)(x - (int64_t)i * units);
+      if (i >= a.keep) continue;
       const int64_t src = row_at(kb, from, h, kept[i]) * units + c;
-      xk[u] = k[src];
-      if (VALUES) xv[u] = v[src];
+      xk[u] = __builtin_nontemporal_load(k + src);
+      if (VALUES) xv[u] = __builtin_nontemporal_load(v + src);
       dst[u] = row_at(kb, to, h, i) * units + c;
     }
 #pragma unroll
@@ -315,7 +476,7 @@ struct Held {
   float scale[PASSES];  // 0 for a row that is not there
 
   __device__ __forceinline__ void load(int p, const void* pool, const float* scales, int64_t row, int64_t at, int shift) {
-    x[p] = *reinterpret_cast<const codes16*>(static_cast<const uint8_t*>(pool) + at);
+    x[p] = __builtin_nontemporal_load(reinterpret_cast<const codes16*>(static_cast<const uint8_t*>(pool) + at));
     scale[p] = scales[row >> shift];
   }
   // The largest finite magnitude, as bits.  Among codes: one more than the
@@ -354,6 +515,7 @@ __global__ void __launch_bounds__(64 * (W > 4 ? W : 4)) move_blocks_kernel(Evict
   if (part == 0 && h == 0) set_length(a, b);
   const int32_t* const kept = a.kept + ((int64_t)b * kb.s.Hkv + h) * a.keep;
   if (kept[0] < 0) return;
+  move_weights(a, (int64_t)b * kb.s.Hkv + h, kept, part, parts);
   const int32_t* const from = kb.table + (int64_t)b * kb.max_pages;
   const int32_t* const to = a.dst_table + (int64_t)b * a.dst_max_pages;
   const int blocks = (a.keep + (1 << SHIFT) - 1) >> SHIFT, column = 16 * (lane % LPR);
@@ -422,6 +584,28 @@ hipError_t by_block(const EvictArgs& a, hipStream_t st) {
   return run_blocks<D, 32, 8>(a, st);
 }
 
+hipError_t run_select(const EvictArgs& a, hipStream_t st) {
+  const kda_kv_shape& s = a.kb.s;
+  const int64_t longest = (int64_t)a.kb.max_pages << a.kb.page_shift, parts = (longest + kShort - 1) / kShort;
+  const dim3 rows((unsigned)(s.B * s.Hkv));
+  if (parts >= kFewestParts && rows.x <= kMostRows && parts * rows.x <= kMostParts && Parts::words(parts) <= a.stride) {
+    const dim3 grid(rows.x, (unsigned)parts);
+    hipLaunchKernelGGL((hist_kernel<0>), grid, dim3(kSelect), 0, st, a, (int)parts);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((hist_kernel<1>), grid, dim3(kSelect), 0, st, a, (int)parts);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL((hist_kernel<2>), grid, dim3(kSelect), 0, st, a, (int)parts);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL(places_kernel, grid, dim3(kSelect), 0, st, a, (int)parts);
+  } else if (longest > kShort) {
+    hipLaunchKernelGGL((select_kernel<true>), rows, dim3(kSelect), 0, st, a);
+  } else {
+    hipLaunchKernelGGL((select_kernel<false>), rows, dim3(kSelect), 0, st, a);
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_kv_evict(const KvBatch& b, const BlockScales& scales, const float* weights, int64_t stride,
@@ -429,17 +613,12 @@ hipError_t launch_kv_evict(const KvBatch& b, const BlockScales& scales, const fl
                            int64_t* new_len, float* new_weights, int32_t* kept, hipStream_t st) {
   const EvictArgs a{b, scales, weights, stride, keep, recent, dst_table, dst_max_pages, new_len, new_weights, kept};
   const kda_kv_shape& s = b.s;
-  const dim3 rows((unsigned)(s.B * s.Hkv));
-  if (((int64_t)b.max_pages << b.page_shift) > kShort)
-    hipLaunchKernelGGL((select_kernel<true>), rows, dim3(kSelect), 0, st, a);
-  else
-    hipLaunchKernelGGL((select_kernel<false>), rows, dim3(kSelect), 0, st, a);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = run_select(a, st);
   if (e != hipSuccess) return e;
   if (scales.k) return s.dk == 128 ? by_block<128>(a, st) : by_block<64>(a, st);
   const int es = s.cache_dtype == KDA_F32 ? 4 : s.cache_dtype == KDA_BF16 ? 2 : 1;
   const int units = s.dk * es / 16;
-  int64_t parts = ((int64_t)keep * units + 4 * kMove - 1) / (4 * kMove);
+  int64_t parts = ((int64_t)keep * units + kAtOnce * kMove - 1) / (kAtOnce * kMove);
   const int64_t most = (((int64_t)1 << 32) - 1) / ((int64_t)s.B * s.Hkv * kMove);
   if (parts > most) parts = most;
   const dim3 grid((unsigned)(s.B * parts), s.Hkv);

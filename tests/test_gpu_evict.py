@@ -157,6 +157,27 @@ def test_long_and_many(kda):
     c.check(3)
 
 
+@pytest.mark.parametrize("name", WEIGHTS)
+@pytest.mark.parametrize("lens,keep,recent", [([50000, 8000, 100], 200, 150), ([41000, 8193, 16384, 30000], 8000, 0),
+                                              ([70000], 60000, 60000), ([65536, 65537], 8192, 1)])
+def test_long_tables(kda, name, lens, keep, recent):
+    """Rows shared out to several workgroups, among them short ones, and parts that end at a row's candidates."""
+    c = Cut("e4m3_d64", lens, keep, Hkv=1, page=128, seed=5, weights=WEIGHTS[name])
+    c.run(kda, recent)
+    c.check(recent)
+    assert c.b.err.item() == 0
+
+
+def test_long_tables_refusals(kda):
+    c = Cut("e4m3_d64", [50000, 50000, 45000, 9000], 9000, Hkv=2, page=128, seed=6, extra=0)
+    c.b.table[0, 70] = -1
+    c.len[1] = c.b.table.shape[1] * 128 + 1
+    c.lens[1] = c.len[1].item()
+    c.run(kda, 100)
+    assert c.b.err.item() == kda.DEV_ERR_PAGE
+    c.check(100, refused=(0, 1))
+
+
 def test_lengths_in_place(kda):
     c = Cut("bf16_d64", [70, 20, 21], 20, seed=6)
     c.run(kda, 5, new_len=c.len)
