@@ -58,11 +58,12 @@ __device__ __forceinline__ Places places_of(const BlocksArgs& a, int b) {
   return s;
 }
 
-// One block's part of a sequence: places [lo, hi), whose block begins at `begin`.
+// One block's part of a sequence: places [lo, hi), whose block begins at `begin`;
+// token row row0 + i is at place begin + i (row0 itself may be none).
 struct Item {
   int b;
   int32_t row0, lo, hi, begin;
-  int64_t pos;
+  int32_t total;  // of all items, where the scan came to the last; else INT32_MAX
 };
 // Called by a whole wave; false: there is no item `item`.
 __device__ __forceinline__ bool find_item(const BlocksArgs& a, int item, Item& it) {
@@ -77,12 +78,11 @@ __device__ __forceinline__ bool find_item(const BlocksArgs& a, int item, Item& i
       const int nth = item - before - __builtin_amdgcn_readlane(upto - s.blocks, at);
       const int first = __builtin_amdgcn_readlane(s.first, at), end = __builtin_amdgcn_readlane(s.end, at);
       it.b = c + at;
-      it.row0 = __builtin_amdgcn_readlane(s.row0, at);
-      it.pos = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(s.pos >> 32), at) << 32 |
-                         (uint32_t)__builtin_amdgcn_readlane((int)s.pos, at));
       it.begin = ((first >> a.scales.shift) + nth) << a.scales.shift;
+      it.row0 = it.begin + __builtin_amdgcn_readlane((int32_t)((uint32_t)s.row0 - (uint32_t)s.pos), at);
       it.lo = max(first, it.begin);
       it.hi = min(end, it.begin + (1 << a.scales.shift));
+      it.total = c + kWave < B ? INT32_MAX : before + sum;
       return true;
     }
     before += sum;
@@ -97,7 +97,11 @@ struct Raw16 {
 
 // W waves to a (block, kind); NW waves to a workgroup, which takes every
 // gridDim.y-th set of kinds of its item.  The angles of the item's rows stay in
-// registers, and the next kind's values are asked for before this one's are used.
+// registers, and the next kind's values are asked for before this one's are used
+// (each kind's angles read anew and no loads ahead: 484 us for 300, see below).
+// Large calls are bound by memory: 8 prompts of 8192 tokens, 8 kv heads and 32 query
+// heads of 128, 1.48 GB, 300 us (4.9 TB/s; a copy of 768 MiB 5.3).  Small ones by the
+// chain of loads: lengths, page, old scale, codes.
 template <int D, int W, bool NT, bool AXES>
 __global__ void __launch_bounds__(64 * (W > 4 ? W : 4)) append_blocks_kernel(BlocksArgs a) {
   constexpr int NW = W > 4 ? W : 4, SETS = NW / W;
@@ -117,9 +121,11 @@ __global__ void __launch_bounds__(64 * (W > 4 ? W : 4)) append_blocks_kernel(Blo
       const int err = places_of(a, b).err;
       if (err) set_err(kb.dev_err, err);
     }
-  // The grid covers all items but where ranges overlap.
+  // The grid covers all items but where ranges overlap; where the count of items
+  // is known, no scan says so (KEEP or not: the count takes registers too).
   Item it;
-  for (int item = blockIdx.x; find_item(a, item, it); item += gridDim.x) {
+  it.total = INT32_MAX;
+  for (int item = blockIdx.x; (!KEEP || item < it.total) && find_item(a, item, it); item += gridDim.x) {
     const int32_t page = kb.table[(int64_t)it.b * kb.max_pages + (it.begin >> kb.page_shift)];
     // The lane's rows: token row, and place counted from the block's first.
     int32_t row[PASSES], slot[PASSES];
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(64 * (W > 4 ? W : 4)) append_blocks_kernel(Blo
       const int p = it.lo + part * 16 + i * RPP + lane / LPR;
       live[i] = p < it.hi;  // others stand for the first row, and are not stored
       slot[i] = (live[i] ? p : it.lo) - it.begin;
-      row[i] = (int32_t)(it.row0 + (it.begin + slot[i] - it.pos));
+      row[i] = it.row0 + slot[i];
     }
     auto fetch = [&](int kind, Raw16 (&x)[PASSES]) __attribute__((always_inline)) {
       if (kind >= a.kinds) return;
@@ -312,7 +318,13 @@ hipError_t launch_kv_append_blocks(const KvBatch& b, const BlockScales& scales, 
                                    void* q_out, int64_t q_out_stride, const kda_rotation& rot, const Axes& axes,
                                    hipStream_t st) {
   const BlocksArgs a{b, scales, k, v, q, q_out, q_out_stride, rot, 2 * b.s.Hkv + (q.p ? b.s.Hq : 0), axes};
-  return b.s.dk == 128 ? by_rows<128, false>(a, st) : by_rows<64, false>(a, st);
+  // Calls that touch more than the 256 MB Infinity Cache go past it, as the plain
+  // append's do (2 + 2 bytes for a query's value, 2 + 1 for a key's):
+  // 8 prompts of 8192 tokens 300 us for 316, 64 sequences of 4 tokens 7.9 either way.
+  const int64_t bytes = b.n_tokens * b.s.dk * (3 * 2 * b.s.Hkv + (q.p ? 4 * b.s.Hq : 0));
+  const bool large = bytes > (int64_t)256 << 20;
+  if (b.s.dk == 128) return large ? by_rows<128, true>(a, st) : by_rows<128, false>(a, st);
+  return large ? by_rows<64, true>(a, st) : by_rows<64, false>(a, st);
 }
 
 }  // namespace kda

@@ -147,6 +147,45 @@ def test_one_call_or_many_give_the_same_values(kda):
         assert (d[x.float().abs() >= 2.0 ** -5] == 0).all() and d.max() <= 2.0 ** -8
 
 
+@pytest.mark.parametrize("width,block,T", [(128, 16, 12400), (128, 256, 12400), (64, 32, 24700), (128, 64, 4)])
+def test_large_calls_write_what_small_ones_do(kda, width, block, T):
+    """Calls past the size of the caches, against the same sequences in calls of at most 4096 tokens: bit for bit."""
+    dev, B, Hq, Hkv, page = torch.device("cuda"), max(1, 12400 // T), 32, 8, 256
+    if T == 4:  # many sequences, as in a round of drafts; 5 calls of a part of them each
+        page = 64
+    g = torch.Generator(device=dev).manual_seed(block)
+    per = -(-T // page)
+    n_pages = B * per
+    qkv = torch.randn(B * T, (Hq + 2 * Hkv) * width, generator=g, device=dev).bfloat16()
+    q, k, v = (x.unflatten(1, (-1, width)) for x in qkv.split([Hq * width, Hkv * width, Hkv * width], 1))
+    assert qkv.numel() // qkv.shape[1] * width * (6 * Hkv + 4 * Hq) > 256 << 20
+    cos_sin = torch.randn(T, width, generator=g, device=dev)
+    table = torch.arange(n_pages, dtype=torch.int32, device=dev).view(B, per)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    got = []
+    for at_once in (B * T, 4096):
+        side = lambda: (torch.zeros(n_pages, Hkv, page, width, device=dev).to(torch.float8_e4m3fn),  # noqa: E731
+                        torch.full((n_pages, Hkv, page // block), 2.0 ** -64, device=dev))
+        (kp, ks), (vp, vs) = side(), side()
+        pool = kda.PagePool.from_tensors(kp, vp, k_scale=ks, v_scale=vs, scale_block=block)
+        out = torch.empty(B * T, Hq, width, dtype=torch.bfloat16, device=dev)
+        if B == 1:
+            calls = [(0, B, x, min(x + at_once, T)) for x in range(0, T, at_once)]
+        else:
+            calls = [(b, min(b + at_once // T, B), 0, T) for b in range(0, B, at_once // T)]
+        for b0, b1, t0, t1 in calls:
+            rows, n = slice(b0 * T + t0, (b1 - 1) * T + t1), t1 - t0
+            start = torch.arange(0, (b1 - b0) * n + 1, n, dtype=torch.int32, device=dev)
+            pos = torch.full((b1 - b0,), t0, dtype=torch.int64, device=dev)
+            kda.kv_append(pool, table[b0:b1], pos, k[rows], v[rows], err, q=q[rows], q_out=out[rows], cos_sin=cos_sin,
+                          tok_start=start, T=n)
+        torch.cuda.synchronize()
+        got.append((out, kp.view(torch.uint8), ks, vp.view(torch.uint8), vs))
+    assert err.item() == 0
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
 def test_rejected_drafts_are_written_over(kda):
     b = BlockBatch(64, 16, Hq=2, Hkv=1, page=16, pos=[5], counts=[6], seed=12, extra_cols=1)
     b.table[b.table < 0] = 0
