@@ -36,7 +36,6 @@ constexpr float kLn2 = 0.69314718055994530942f;
 
 struct AttnArgs {
   KvBatch kb;
-  BlockScales scales;
   KvRows q;
   float scale;
   int32_t window;
@@ -51,9 +50,10 @@ struct AttnArgs {
   // Workspace: each sequence's first and last worker [B], then for every piece
   // (worker, slot, kv head, row block) its rows' (max, sum) and outputs.  A sum
   // below zero refuses the sequence.
-  int2* span;  // null: no pieces are joined
+  int2* span;
   f32x2* piece_ml;
   float* piece_o;
+  BlockScales scales;
 };
 
 __device__ __forceinline__ int64_t piece_index(const AttnArgs& a, int worker, int slot, int hk, int rb) {
@@ -139,7 +139,8 @@ struct Shares {
 
 // A worker's run [tile, end) of the list, and the sequence that it is at: number
 // b, whose own tiles begin at `first`.
-template <int TILE>
+// JOINED: pieces of sequences are joined after the call.
+template <int TILE, bool JOINED = true>
 struct Run {
   const AttnArgs& a;
   int32_t tile, end, first;
@@ -215,7 +216,7 @@ struct Run {
       upto = wave_scan(count);
       if (__builtin_amdgcn_readlane(upto, kWave - 1) <= a.workers) break;
     }
-    if (record && a.span && lane < a.kb.s.B) a.span[lane] = make_int2(upto - count, max(upto - 1, upto - count));
+    if (JOINED && record && lane < a.kb.s.B) a.span[lane] = make_int2(upto - count, max(upto - 1, upto - count));
     const uint64_t past = __ballot(upto > worker);
     if (past == 0) return;
     b = __ffsll((unsigned long long)past) - 1;
@@ -231,7 +232,7 @@ struct Run {
 
   // Sequence `seq`, whose tiles end before place `upto`.
   __device__ __forceinline__ void write_span(const Shares& shares, int seq, int32_t upto, int32_t tiles) const {
-    if (a.span && seq < a.kb.s.B)
+    if (JOINED && seq < a.kb.s.B)
       a.span[seq] = tiles > 0 ? make_int2(shares.of(upto - tiles), shares.of(upto - 1)) : make_int2(0, 0);
   }
 
@@ -450,16 +451,16 @@ inline Workspace workspace_of(const kda_kv_shape& s, const Split& d) {
   return L;
 }
 
-inline AttnArgs make_args(const KvBatch& b, const BlockScales& scales, KvRows q, float scale, int32_t window, void* o, float* lse,
-                          void* workspace, const Split& d) {
+inline AttnArgs make_args(const KvBatch& b, const BlockScales& scales, KvRows q, float scale, int32_t window, void* o,
+                          float* lse, void* workspace, const Split& d) {
   const Workspace L = workspace_of(b.s, d);
   char* ws = static_cast<char*>(workspace);
-  return AttnArgs{b, scales, q,
+  return AttnArgs{b,         q,
                   scale,     window,
                   o,         lse,
                   d.workers, d.run_tiles, d.start_tiles, d.few, d.row_blocks,
                   d.rows,    reinterpret_cast<int2*>(ws),
-                  reinterpret_cast<f32x2*>(ws + L.ml), reinterpret_cast<float*>(ws + L.o)};
+                  reinterpret_cast<f32x2*>(ws + L.ml), reinterpret_cast<float*>(ws + L.o), scales};
 }
 
 // The join after an attention kernel.  A sequence has about workers / B pieces

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : 2) tokens_kernel
   const KvBatch& kb = a.kb;
   const int wave = uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4;
   const int hk = blockIdx.y, worker = blockIdx.x;
-  Run<TILE> run(a, worker, worker == 0 && hk == 0 && wave == 0);
+  Run<TILE, false> run(a, worker, worker == 0 && hk == 0 && wave == 0);
   const float x_scale = x_scale_of<TC, BLK>(a, hk);
   // Lane group u holds the sums of tokens 16 u + (lane & 15) of a tile.
   const int group = min(g, GROUPS - 1), mine = 16 * group + (lane & 15);
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kWaves * kWave, (kRowsWaves<D, TIn, NQ>)) rows
   const KvBatch& kb = a.kb;
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, g = lane >> 4;
   const int hk = blockIdx.y, worker = blockIdx.x;
-  Run<TILE> run(a, worker, worker == 0 && hk == 0 && wave == 0);
+  Run<TILE, false> run(a, worker, worker == 0 && hk == 0 && wave == 0);
   const float x_scale = x_scale_of<TC, BLK>(a, hk);
   const int group = min(g, GROUPS - 1), mine = 16 * group + (lane & 15);
   // The loads of this wave are of one group of 16 rows.
