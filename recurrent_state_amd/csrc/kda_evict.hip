@@ -304,16 +304,20 @@ struct Parts {
   // Words of a row that this takes; no more than a row of (parts - 1) kShort has, from three parts on.
   static constexpr int64_t words(int64_t parts) { return parts * (2048 + 2048 + 1024 + 1) + 4; }
 
-  // The sum of a digit's histograms of the row's parts to lds.hist.
-  __device__ __forceinline__ void add_up(int digit, int count, SelectLds& lds) const {
-    uint32_t c[2] = {0, 0};
+  // The sum of a digit's histograms of the row's parts to lds.hist.  Returned: that
+  // of the parts before `part`, of the thread's bin.
+  __device__ __forceinline__ uint32_t add_up(int digit, int count, SelectLds& lds, int part) const {
+    uint32_t c[2] = {0, 0}, before = 0;
     const uint32_t* p = hist[digit] + threadIdx.x;
 #pragma unroll 8
     for (int i = 0; i < count; ++i) {
-      c[0] += p[i * kBinsOf[digit]];
+      const uint32_t x = p[i * kBinsOf[digit]];
+      c[0] += x;
+      before += i < part ? x : 0;
       if (digit < 2) c[1] += p[i * kBinsOf[digit] + kSelect];
     }
     lds.hist[threadIdx.x] = c[0], lds.hist[threadIdx.x + kSelect] = c[1];
+    return before;
   }
 };
 
@@ -349,7 +353,7 @@ __global__ void __launch_bounds__(kSelect) hist_kernel(EvictArgs a, int parts) {
   const Stretch mine(r, part);
   uint32_t top = 0;
   if (DIGIT > 0) {
-    p.add_up(DIGIT - 1, (r.n + kShort - 1) / kShort, lds);
+    p.add_up(DIGIT - 1, (r.n + kShort - 1) / kShort, lds, 0);
     find_digit(lds, DIGIT == 1 ? 0 : p.row[1], r.k);
     top = DIGIT == 1 ? lds.found[0] : p.row[0] << 11 | lds.found[0];
     if (part == 0 && tid == 0) p.row[2 * DIGIT - 2] = top, p.row[2 * DIGIT - 1] = lds.found[1];
@@ -382,7 +386,7 @@ __global__ void __launch_bounds__(kSelect) places_kernel(EvictArgs a, int parts)
   if (r.bad || r.stays || r.k == 0 || part * kShort >= r.n) return;
   const Parts p(r, parts);
   const Stretch mine(r, part);
-  p.add_up(2, (r.n + kShort - 1) / kShort, lds);
+  const uint32_t before = p.add_up(2, (r.n + kShort - 1) / kShort, lds, part);
   find_digit(lds, p.row[3], r.k);
   const uint32_t digit = lds.found[0], top = p.row[2] << 10 | digit, equal = (uint32_t)r.k - lds.found[1];
   // Kept ones of the parts before this, then of the waves.
@@ -390,8 +394,7 @@ __global__ void __launch_bounds__(kSelect) places_kernel(EvictArgs a, int parts)
   if (tid == 0) lds.found[0] = lds.found[1] = 0;
   __syncthreads();
   uint32_t gt = tid < part ? p.gt[tid] : 0, eq = tid < part ? p.hist[2][tid * 1024 + digit] : 0;
-  if ((uint32_t)tid > digit)
-    for (int i = 0; i < part; ++i) gt += p.hist[2][i * 1024 + tid];
+  if ((uint32_t)tid > digit) gt += before;
   if (gt) atomicAdd(&lds.found[0], gt);
   if (eq) atomicAdd(&lds.found[1], eq);
   gt = eq = 0;
