@@ -765,11 +765,12 @@ kda_status kda_attn_weights(const kda_kv_shape* shape, const kda_pages* pages, c
  *   weights        f32 [B][Hkv][weights_stride], as above; finite or not
  *   new_weights    the same layout: those of the kept tokens (of all tokens of a
  *                  sequence that stays) at their places, and 0 from new_len[b] on
- *                  to weights_stride.  Must not overlap weights.
+ *                  to weights_stride.  Must not overlap weights (KDA_ERR_SHAPE).
  *   kept           device int32 [B][Hkv][keep]: the places that the tokens came
  *                  from, ascending
  * Destination pages must be pages of this pool that no table row of the call
- * names as a source, each used once.  With scales, a block's new scale is the
+ * names as a source, each used once; dst_table equal to table is refused
+ * (KDA_ERR_SHAPE).  With scales, a block's new scale is the
  * one that kda_kv_append_blocks gives to its values; without, rows are copied
  * bit for bit (grouped or latent form).  shape gives B, Hkv, dk, dv and
  * cache_dtype; its T, Hq and in_dtype have to be valid, no more.  keep is at

@@ -877,6 +877,10 @@ kda_status kda_kv_evict(const kda_kv_shape* shape, const kda_pages* pages, const
   if (!aligned(weights, 4) || !aligned(dst_table, 4) || !aligned(new_len, 8) || !aligned(new_weights, 4) ||
       !aligned(kept, 4))
     return KDA_ERR_ALIGN;
+  // The choice reads weights while new_weights is written, the move one table's pages while it writes the other's.
+  const uintptr_t w0 = reinterpret_cast<uintptr_t>(weights), w1 = reinterpret_cast<uintptr_t>(new_weights);
+  if ((w0 < w1 ? w1 - w0 : w0 - w1) / 4 < (uint64_t)weights_stride * s.B * s.Hkv || dst_table == table)
+    return KDA_ERR_SHAPE;
   return launched(kda::launch_kv_evict(b, bs, weights, weights_stride, keep, recent, dst_table, dst_max_pages, new_len,
                                        new_weights, kept, static_cast<hipStream_t>(stream)),
                   KDA_VARIANT_KV_EVICT);

@@ -143,6 +143,11 @@ def test_evict_arguments(k):  # noqa: F811
         assert evict(k, **bad) == SHAPE, bad
     assert evict(k, shp(k, B=1 << 18, T=1 << 10, Hq=8, Hkv=8)) == SHAPE
     assert evict(k, shp(k, Hkv=1, dk=576, dv=512), pages(k, vp=None), w=None) == NULL   # latent pools are taken
+    # new_weights in weights (B * Hkv * stride floats), and a table that names its own pages.
+    s, at = shp(k, B=2, T=1, Hq=8, Hkv=4), lambda i: type(GOOD)(GOOD.value + i)  # noqa: E731
+    for i in (0, 4 * 8 * 512 - 4, 4 - 4 * 8 * 512):
+        assert evict(k, s, new_w=at(i), stride=512, dst=at(4096)) == SHAPE
+    assert evict(k, s, new_w=at(4 * 8 * 512), stride=512) == SHAPE
     assert evict(k, shp(k, Hkv=1, dk=576, dv=512)) == SHAPE
     none = dict(table=None, len=None, w=None, dst=None, new_len=None, new_w=None, kept=None, err=None)
     assert evict(k, shp(k, B=0), pages(k, None, None), **none) == OK
