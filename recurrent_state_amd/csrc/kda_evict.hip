@@ -8,13 +8,13 @@
 //           above.  Then every wave counts, in its own stretch of tokens, those
 //           above it and those equal to it, and after one scan over the waves
 //           writes its kept places in order.  Bound by the passes' latency:
-//           8 heads' 100001 tokens take 27 us in parts, 64 by one workgroup each;
+//           8 heads' 100001 tokens take 26 us in parts, 64 by one workgroup each;
 //           64 sequences of up to 8191 tokens, 8 heads, 15 us.
 //   move    Rows go from their places to the new ones.  Pages without scales or
 //           with scales by heads are copied 16 bytes to a thread; where scales go
 //           by blocks, a group of waves takes a new block, whose scale is that of
 //           its largest value.  Bound by memory: 20000 tokens of 8 heads of 128 in
-//           bf16 32 us (5.2 TB/s), those 64 sequences cut to 2000 e4m3 tokens 60.
+//           bf16 32 us (5.2 TB/s), those 64 sequences cut to 2000 e4m3 tokens 58.
 
 #include "kda_blocks.h"
 
@@ -505,8 +505,11 @@ struct Held {
   }
 };
 
-// A wave takes up to 32 rows of a new block, keys and values together, so that many
-// loads are on their way; W waves to a block, NW to a workgroup.
+// A wave takes 16 or 32 rows of a new block, keys and values together, so that many
+// loads are on their way; W waves to a block, NW to a workgroup.  16 rows leave the
+// chip more waves, but waves of a block wait for each other: of 64 sequences the
+// whole call into blocks of 32 takes 76 us with 16 rows and 78 with 32, of 64
+// 76 and 78, of 128 80 and 78.
 template <int D, int ROWS, int W>
 __global__ void __launch_bounds__(64 * (W > 4 ? W : 4)) move_blocks_kernel(EvictArgs a, int parts) {
   constexpr int NW = W > 4 ? W : 4, BLOCKS = NW / W, SHIFT = __builtin_ctz(ROWS * W);
@@ -580,8 +583,8 @@ template <int D>
 hipError_t by_block(const EvictArgs& a, hipStream_t st) {
   switch (a.scales.shift) {
     case 4: return run_blocks<D, 16, 1>(a, st);
-    case 5: return run_blocks<D, 32, 1>(a, st);
-    case 6: return run_blocks<D, 32, 2>(a, st);
+    case 5: return run_blocks<D, 16, 2>(a, st);
+    case 6: return run_blocks<D, 16, 4>(a, st);
     case 7: return run_blocks<D, 32, 4>(a, st);
   }
   return run_blocks<D, 32, 8>(a, st);
