@@ -733,7 +733,8 @@ kda_status kda_attn_decode_blocks(const kda_kv_shape* shape, const kda_pages* pa
  * to before; those of a prompt that no call weighs begin with what the caller
  * put there).  Tokens that no row sees are left as they are.
  *   q, lse   the queries given to kda_attn_decode and the lse that it returned
- *            (f32 [n_tokens][Hq]), with the same scale and window
+ *            (f32 [n_tokens][Hq]), with the same scale and window; of more
+ *            tokens than that takes at once, from several of its calls
  *   weights  f32 [B][Hkv][weights_stride], weights_stride (floats) at least
  *            max_pages * page_size
  * Grouped form; scales NULL: pages as kda_attn_decode, else as

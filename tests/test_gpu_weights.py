@@ -100,6 +100,22 @@ def test_rows_and_windows(kda, form, hq, hkv, T, window):
     check(b, before, window=window)
 
 
+@pytest.mark.parametrize("hq,hkv,T", [(8, 1, 5), (4, 2, 40), (8, 2, 70), (16, 1, 128)])
+@pytest.mark.parametrize("form", GROUPED + ["blocks_d64", "blocks_d128"])
+def test_many_rows(kda, form, hq, hkv, T):
+    """More rows than a wave holds, in every form: tiles past the ring of sums, sequences of one tile, of a few, of none."""
+    counts = [T, 0, T - 1, 1, T]
+    b = prepared(batch(form, Hq=hq, Hkv=hkv, page=64, pos=[0, 9, 700, 1290, 31], counts=counts, seed=3), window=900)
+    before = b.w.clone()
+    run(kda, b, window=900)
+    check(b, before, window=900)
+    assert b.err.item() == 0
+    again = b.w.clone()
+    b.w.copy_(before)
+    run(kda, b, window=900)
+    assert torch.equal(b.w, again)
+
+
 def test_two_calls_add_up(kda):
     b = prepared(batch("bf16_d64", Hq=4, Hkv=2, page=16, pos=[40, 9], counts=[1, 1], seed=3, extra_cols=1))
     b.table[b.table < 0] = 0
@@ -180,6 +196,26 @@ def test_splits(kda, B, tokens):
     b.w.zero_()
     run(kda, b)
     assert torch.equal(b.w, again)
+
+
+@pytest.mark.parametrize("form", ["bf16_d128", "blocks_d64"])
+@pytest.mark.parametrize("B,tokens,T", [(1, 20000, 64), (20, 1500, 33), (150, 80, 17)])
+def test_splits_of_many_rows(kda, form, B, tokens, T):
+    b = batch(form, Hq=8, Hkv=2, page=64, pos=[max(0, tokens - 7 * i) for i in range(B)], counts=[T] * B, seed=8)
+    pool, q = b.pool(kda), b.dense(b.q)
+    ws, lse = kda.attn_workspace(pool, b.table, Hq=8, T=16), []
+    for t in range(0, T, 16):  # the attention takes 16 tokens of a sequence at most
+        part = q[:, t:t + 16].contiguous()
+        lse.append(torch.empty(part.shape[:3], device=b.device))
+        kda.attn_decode(pool, b.table, b.pos + t, part, torch.empty_like(part), ws, b.err, lse=lse[-1])
+    b.lse = torch.cat(lse, 1).flatten(0, 1)
+    b.w = torch.zeros((B, 2, b.table.shape[1] * b.page), device=b.device)
+    run(kda, b)
+    # Four query heads to a kv head and T rows of each, weights that sum to one.  Each comes from two sums of dk
+    # products in fp32, whose orders differ: scores of up to about 8 times 2 dk 2^-24 twice.
+    assert (b.w.double().sum(-1) - 4 * T).abs().max() < 4 * T * 2 * 8 * 2 * b.dk * 2.0 ** -24
+    j = torch.arange(b.w.shape[-1], device=b.device)
+    assert ((b.w > 0) == (j < b.pos[:, None] + T)[:, None]).all()
 
 
 def test_strided_queries_and_another_stream(kda):
