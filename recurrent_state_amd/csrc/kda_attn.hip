@@ -25,7 +25,12 @@
 // fp32 caches take the same paths through v_mfma_f32_16x16x4_f32 (no
 // permutations: an operand is one value per lane); e4m3 values are widened to
 // bf16, which holds each of them exactly, and their scales enter the softmax
-// scale and the result.
+// scale and the result.  Where scales go by blocks of tokens (a group of 16 lies in
+// one block), a key's joins the factor of its scores and a value's its
+// probabilities, before these are rounded: four numbers more to a tile and wave,
+// loaded with the rows.  64 sequences of 60 to 8191 tokens with 0 to 4 drafts take
+// 48 us so and 49 with a scale a head, one of 131071 tokens 53 (269 MB, 5.7 TB/s in
+// the kernel, 6 us the join).
 //
 // Measured with the join, 32 heads over 8 of 128, one new token each: one
 // sequence of 131071 tokens 92 us (537 MB, 5.8 TB/s), 64 of 60 to 8191 tokens
