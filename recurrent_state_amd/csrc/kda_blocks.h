@@ -40,7 +40,15 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
   return x;
 }
 
-// Codes times f (at most 1), rounded to nearest even; NaN stays NaN.
+// What codes of scale `old` are multiplied by under the new one, s.  In an append
+// that is at most 1; a moved row's new block may have a scale 2^184 times less,
+// where the row is all zeros (any other code's value is at most 448 s).  The factor
+// then ends at fp32's largest, since 0 times infinity would be NaN.
+__device__ __forceinline__ float factor(float old, uint32_t s) {
+  const float f = old * inverse(s), most = __uint_as_float(kLargest);
+  return magnitude(old) <= kLargest ? fminf(fmaxf(f, -most), most) : f;
+}
+// Codes times f, rounded to nearest even; NaN stays NaN.
 __device__ __forceinline__ codes16 rescaled(codes16 x, float f) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
