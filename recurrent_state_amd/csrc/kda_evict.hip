@@ -482,9 +482,10 @@ struct Held {
     x[p] = __builtin_nontemporal_load(reinterpret_cast<const codes16*>(static_cast<const uint8_t*>(pool) + at));
     scale[p] = scales[row >> shift];
   }
-  // The largest finite magnitude, as bits.  Among codes: one more than the
-  // magnitude's, which orders as the values do and sends NaN (0x7f) to 0; two
-  // bytes at a time.
+  // The largest finite magnitude, as bits; one past fp32's largest counts as that
+  // (256 at 2^120 is 2^128, and what an append makes of the largest fp32 values).
+  // Among codes: one more than the magnitude's, which orders as the values do and
+  // sends NaN (0x7f) to 0; two bytes at a time.
   __device__ __forceinline__ uint32_t top() const {
     typedef __attribute__((ext_vector_type(2))) uint16_t u16x2;
     uint32_t m = 0;
@@ -499,7 +500,7 @@ struct Held {
       }
       const int code = max((int)most[0], (int)most[1]);
       const float value = code ? __builtin_amdgcn_cvt_f32_fp8(code - 1, 0) : 0.f;
-      m = max(m, finite_bits(value * scale[p]));
+      m = max(m, magnitude(scale[p]) <= kLargest ? min(magnitude(value * scale[p]), kLargest) : 0);
     }
     return m;
   }

@@ -59,3 +59,12 @@ def test_rows_of_zeros_beside_small_ones(kda, seed):
     c.before = [x.clone() for x in (b.k_pages, b.v_pages, b.k_scale, b.v_scale)]
     c.run(kda, 3)
     c.check(3)
+
+
+@pytest.mark.parametrize("exps", [[120], [118, 119, 120], [-64, 120]])
+@pytest.mark.parametrize("codes", [[0x78, 0xf8], [0x77, 0x78, 0x7e, 0x00, 0xfe], list(range(0x7f)) + [0x7f]])
+def test_values_past_fp32_count_for_the_scale(kda, exps, codes):
+    """256 at a scale of 2^120, which an append of the largest fp32 values stores, is 2^128: the block needs 2^120."""
+    c = cut(exps, codes, 37)
+    c.run(kda, 5)
+    c.check(5)
