@@ -692,9 +692,10 @@ typedef struct kda_block_scales {
  * that the call puts into a block of a kv head (keys, rotated, and values
  * apart), the block needs the scale
  *   2^e, e the least integer with m <= 448 * 2^e, but at least -64.
- * A block whose first token is new gets that scale.  One that holds earlier
- * tokens of the sequence (the call begins inside it) gets the larger of that
- * and its scale so far, rounded up to a power of two; where this raises it, the
+ * (e <= 120 for every float).  A block whose first token is new gets that scale.
+ * One that holds earlier tokens of the sequence (the call begins inside it) gets
+ * the larger of that and its scale so far, rounded up to a power of two, and at
+ * most 2^120 (old values past 448 * 2^120 end there); where this raises it, the
  * earlier tokens are rounded anew, to old * (old scale / new scale), which
  * changes only values below 2^-6 new scales (the type's subnormals).  New values
  * are x / scale, clamped to +-448 (infinities too) and rounded to nearest even,
@@ -772,7 +773,8 @@ kda_status kda_attn_weights(const kda_kv_shape* shape, const kda_pages* pages, c
  * Destination pages must be pages of this pool that no table row of the call
  * names as a source, each used once; dst_table equal to table is refused
  * (KDA_ERR_SHAPE).  With scales, a block's new scale is the
- * one that kda_kv_append_blocks gives to its values; without, rows are copied
+ * one that kda_kv_append_blocks gives to its values (of those past the range of
+ * float, 2^120); without, rows are copied
  * bit for bit (grouped or latent form).  shape gives B, Hkv, dk, dv and
  * cache_dtype; its T, Hq and in_dtype have to be valid, no more.  keep is at
  * least 1 and at most dst_max_pages * page_size, weights_stride at least

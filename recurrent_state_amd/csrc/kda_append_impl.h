@@ -59,9 +59,7 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   put<NT>(reinterpret_cast<f32x4*>(p) + 1, (f32x4){x[4], x[5], x[6], x[7]});
 }
 
-// 8 values as e4m3: clamped to the type's largest (it has no infinity; NaN stays
-// NaN) and rounded to nearest even by the conversion.
-__device__ __forceinline__ float to_range(float y) { return y != y ? y : fminf(fmaxf(y, -448.f), 448.f); }
+// 8 values as e4m3, rounded to nearest even by the conversion.
 __device__ __forceinline__ u32x2 e4m3_of(const float (&y)[8]) {  // of values in range
   int w[2] = {0, 0};
 #pragma unroll

@@ -10,7 +10,8 @@ namespace {
 
 typedef __attribute__((ext_vector_type(4))) uint32_t codes16;  // 16 e4m3 values
 
-constexpr uint32_t kLeastScale = (127u - 64) << 23, kMostScale = (127u + 120) << 23;  // 2^-64, 2^120
+// 2^-64 and 2^120; at 2^120 every fp32 value is below 448 scales.
+constexpr uint32_t kLeastScale = (127u - 64) << 23, kMostScale = (127u + 120) << 23;
 
 // |x| as bits, which order as the values do, infinities and then NaN behind
 // kLargest; and with 0 for what is not finite.
@@ -49,14 +50,23 @@ __device__ __forceinline__ float factor(float old, uint32_t s) {
   return magnitude(old) <= kLargest ? fminf(fmaxf(f, -most), most) : f;
 }
 // Codes times f, rounded to nearest even; NaN stays NaN.
-__device__ __forceinline__ codes16 rescaled(codes16 x, float f) {
+template <bool CLAMP>
+__device__ __forceinline__ codes16 times(codes16 x, float f) {
+  const auto in = [](float y) { return CLAMP ? to_range(y) : y; };
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[i], true);
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(lo[0] * f, lo[1] * f, 0, false);
-    x[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(hi[0] * f, hi[1] * f, w, true);
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(in(lo[0] * f), in(lo[1] * f), 0, false);
+    x[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(in(hi[0] * f), in(hi[1] * f), w, true);
   }
   return x;
+}
+// Codes of scale `old` under the scale s, which is at least their block's
+// scale_for().  Only an old one over 2^120 (no call sets such a scale) leaves codes
+// past 448: those of values that fp32 does not hold.
+__device__ __forceinline__ codes16 rescaled(codes16 x, float old, uint32_t s) {
+  const float f = factor(old, s);
+  return magnitude(old) > kMostScale ? times<true>(x, f) : times<false>(x, f);
 }
 
 }  // namespace

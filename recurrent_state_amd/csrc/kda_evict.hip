@@ -562,8 +562,8 @@ __global__ void __launch_bounds__(64 * (W > 4 ? W : 4)) move_blocks_kernel(Evict
       const int i = first + p * RPP;
       if (i >= count) continue;
       const int64_t to_at = (dst + i) * D + column;
-      *reinterpret_cast<codes16*>(static_cast<uint8_t*>(kb.pages.k) + to_at) = rescaled(k.x[p], factor(k.scale[p], sk));
-      *reinterpret_cast<codes16*>(static_cast<uint8_t*>(kb.pages.v) + to_at) = rescaled(v.x[p], factor(v.scale[p], sv));
+      *reinterpret_cast<codes16*>(static_cast<uint8_t*>(kb.pages.k) + to_at) = rescaled(k.x[p], k.scale[p], sk);
+      *reinterpret_cast<codes16*>(static_cast<uint8_t*>(kb.pages.v) + to_at) = rescaled(v.x[p], v.scale[p], sv);
     }
   }
 }

@@ -19,6 +19,9 @@ __device__ __forceinline__ int here(int x) {
   return x;
 }
 
+// A value clamped to e4m3's largest (the type has no infinity); NaN stays NaN.
+__device__ __forceinline__ float to_range(float y) { return y != y ? y : fminf(fmaxf(y, -448.f), 448.f); }
+
 // Inclusive sum over the wave's lanes: inside each 16-lane row by shifts of 1,
 // 2, 4 and 8, then the last lane of a row to the row after it and of the lower
 // half to the upper.  No LDS, no barrier.
