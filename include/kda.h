@@ -714,8 +714,8 @@ kda_status kda_kv_append_blocks(const kda_kv_shape* shape, const kda_pages* page
 
 /*
  * kda_attn_decode over such pages: k_j and v_j are the stored values times the
- * scales of their blocks.  Scales of blocks without a visible token do not
- * matter, whatever they hold.  workspace as kda_attn_workspace_bytes says for
+ * scales of their blocks.  The scale of a block in which a row sees no token does
+ * not reach the row, whatever it holds.  workspace as kda_attn_workspace_bytes says for
  * this shape and pool.
  */
 kda_status kda_attn_decode_blocks(const kda_kv_shape* shape, const kda_pages* pages, const kda_block_scales* scales,

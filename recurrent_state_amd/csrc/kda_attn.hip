@@ -144,15 +144,25 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
         }
       };
       // O^T += V^T P^T, with blocks' scales in the probabilities (powers of two
-      // there lose nothing).
-      auto weigh = [&] {
+      // there lose nothing).  PART: some row does not see some token; its
+      // probability stays zero, whatever the scale is.
+      auto weigh = [&](auto part) {
+        constexpr bool PART = decltype(part)::value;
+        const int g = PART ? here(lane) >> 4 : 0;
         if constexpr (BLK)
 #pragma unroll
-          for (int u = 0; u < GROUPS; ++u)
+          for (int n = 0; n < NQ; ++n) {
+            // The row sees token j: j - first < count, without sign.
+            const uint32_t first = a.window > 0 ? vis[n] - a.window + 1 : 0, count = vis[n] + 1 - first;
+            const uint32_t at = t0 + 4 * g - first;
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
+            for (int u = 0; u < GROUPS; ++u)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) p[n][u][i] *= v_block[u];
+              for (int i = 0; i < 4; ++i) {
+                const float x = p[n][u][i] * v_block[u];
+                p[n][u][i] = !PART || at + 16 * u + i < count ? x : 0.f;
+              }
+          }
         cache.weigh(p, out);
       };
       // Scores to probabilities, and the earlier sums to the new maximum.
@@ -205,7 +215,7 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
           scores();
           load_k(t0 + TILE);
           softmax(std::false_type{});
-          weigh();
+          weigh(std::false_type{});
           load_v();
         }
         scores();
@@ -256,7 +266,7 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
             }
           }
         }
-        weigh();
+        weigh(std::true_type{});
         t0 += TILE;
       }
 
