@@ -145,6 +145,12 @@ struct BlockScales {
 // rot.cos_sin null: keys are stored as they are.  q.p null: no queries.
 hipError_t launch_kv_append(const KvBatch& b, KvRows k, KvRows v, KvRows q, void* q_out, int64_t q_out_stride,
                             const kda_rotation& rot, const Axes& axes, hipStream_t st);
+// Bytes that an append into blocks reads and writes: 2 + 1 for a key's or value's
+// number, 2 + 2 for a query's.  They pass 2^31 from 95326 tokens of 32 + 8 heads of
+// 128 on.
+constexpr int64_t append_blocks_bytes(int64_t n_tokens, const kda_kv_shape& s, bool queries) {
+  return n_tokens * s.dk * (3 * 2 * s.Hkv + (queries ? 4 * s.Hq : 0));
+}
 hipError_t launch_kv_append_blocks(const KvBatch& b, const BlockScales& scales, KvRows k, KvRows v, KvRows q,
                                    void* q_out, int64_t q_out_stride, const kda_rotation& rot, const Axes& axes,
                                    hipStream_t st);

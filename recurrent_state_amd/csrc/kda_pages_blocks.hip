@@ -318,9 +318,9 @@ hipError_t launch_kv_append_blocks(const KvBatch& b, const BlockScales& scales, 
                                    hipStream_t st) {
   const BlocksArgs a{b, scales, k, v, q, q_out, q_out_stride, rot, 2 * b.s.Hkv + (q.p ? b.s.Hq : 0), axes};
   // Calls that touch more than the 256 MB Infinity Cache go past it, as the plain
-  // append's do (2 + 2 bytes for a query's value, 2 + 1 for a key's):
-  // 8 prompts of 8192 tokens 300 us for 316, 64 sequences of 4 tokens 7.9 either way.
-  const int64_t bytes = b.n_tokens * b.s.dk * (3 * 2 * b.s.Hkv + (q.p ? 4 * b.s.Hq : 0));
+  // append's do: 8 prompts of 8192 tokens 300 us for 316, 64 sequences of 4 tokens 7.9
+  // either way.
+  const int64_t bytes = append_blocks_bytes(b.n_tokens, b.s, q.p != nullptr);
   const bool large = bytes > (int64_t)256 << 20;
   if (b.s.dk == 128) return large ? by_rows<128, true>(a, st) : by_rows<128, false>(a, st);
   return large ? by_rows<64, true>(a, st) : by_rows<64, false>(a, st);
