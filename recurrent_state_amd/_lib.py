@@ -771,6 +771,7 @@ class PagePool:
         if scale_block:
             self.c_scales = _BlockScales(k_scale.data_ptr(), v_scale.data_ptr(), scale_block)
 
+
 def _scales(pool):
     """A call's kda_block_scales: None for a pool without scales by blocks."""
     c = getattr(pool, "c_scales", None)
@@ -1078,13 +1079,18 @@ class KvEvictPlan:
         _need(new_weights, "new_weights", weights.shape, torch.float32, dev)
         if kept.dim() != 3:
             raise ValueError(f"kept has shape {tuple(kept.shape)}, expected [B][Hkv][tokens to keep]")
-        _need(kept, "kept", (sh.B, pool.Hkv, kept.shape[2]), torch.int32, dev)
+        keep, room = kept.shape[2], dst_table.shape[1] * pool.page_size
+        _need(kept, "kept", (sh.B, pool.Hkv, keep), torch.int32, dev)
+        if not 1 <= keep <= room:
+            raise ValueError(f"kept names {keep} tokens to keep, expected 1 to the {room} that a row of dst_table holds")
+        if not 0 <= int(recent) <= keep:
+            raise ValueError(f"recent is {recent}, expected 0 to the {keep} tokens to keep")
         _need(dev_err, "dev_err", (1,), torch.int32, dev)
         self._keep = (pool, table, length, weights, dst_table, new_length, new_weights, kept, dev_err, sh)
         self._device = dev
         scales = _scales(pool)
         self._args = (ctypes.byref(sh), ctypes.byref(pool.c), scales, _ptr(table), table.shape[1], _ptr(length),
-                      _ptr(weights), stride, kept.shape[2], int(recent), _ptr(dst_table), dst_table.shape[1],
+                      _ptr(weights), stride, keep, int(recent), _ptr(dst_table), dst_table.shape[1],
                       _ptr(new_length), _ptr(new_weights), _ptr(kept), _ptr(dev_err))
         self._fn = lib().kda_kv_evict
 
@@ -1100,6 +1106,8 @@ def kv_evict(pool: PagePool, table, length, weights, dst_table, new_length, new_
     they go, in order, to the pages of dst_table (int32 [B][pages], pages that no
     sequence of the call has), their sums to new_weights, and their places to
     kept (int32 [B][Hkv][tokens to keep]).  Shorter sequences stay where they are
-    (kept -1).  new_length: int64 [B], may be length itself.  Keyword: recent.
+    (kept -1).  new_length: int64 [B], may be length itself; new_weights may not
+    be weights (the call refuses it), and later attn_weights go on with it.
+    Keyword: recent.
     """
     KvEvictPlan(pool, table, length, weights, dst_table, new_length, new_weights, kept, dev_err, **kw)()
