@@ -41,15 +41,9 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
   return x;
 }
 
-// What codes of scale `old` are multiplied by under the new one, s.  In an append
-// that is at most 1; a moved row's new block may have a scale 2^184 times less,
-// where the row is all zeros (any other code's value is at most 448 s).  The factor
-// then ends at fp32's largest, since 0 times infinity would be NaN.
-__device__ __forceinline__ float factor(float old, uint32_t s) {
-  const float f = old * inverse(s), most = __uint_as_float(kLargest);
-  return magnitude(old) <= kLargest ? fminf(fmaxf(f, -most), most) : f;
-}
-// Codes times f, rounded to nearest even; NaN stays NaN.
+// Codes times f, rounded to nearest even; NaN stays NaN.  CLAMP: products may pass
+// 448, since a scale past 2^120 (no call sets one) stands for values that fp32 does
+// not hold.
 template <bool CLAMP>
 __device__ __forceinline__ codes16 times(codes16 x, float f) {
   const auto in = [](float y) { return CLAMP ? to_range(y) : y; };
@@ -58,15 +52,17 @@ __device__ __forceinline__ codes16 times(codes16 x, float f) {
     const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[i], true);
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(in(lo[0] * f), in(lo[1] * f), 0, false);
     x[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(in(hi[0] * f), in(hi[1] * f), w, true);
+    if (CLAMP) asm volatile("" : "+v"(x[i]), "+v"(f));  // four codes at a time: few registers
   }
   return x;
 }
-// Codes of scale `old` under the scale s, which is at least their block's
-// scale_for().  Only an old one over 2^120 (no call sets such a scale) leaves codes
-// past 448: those of values that fp32 does not hold.
+// Codes of scale `old` in a block that holds other rows too and has the scale s.  That
+// may be 2^184 times less where these are all zeros: the factor ends at fp32's largest,
+// since 0 times infinity would be NaN.
 __device__ __forceinline__ codes16 rescaled(codes16 x, float old, uint32_t s) {
-  const float f = factor(old, s);
-  return magnitude(old) > kMostScale ? times<true>(x, f) : times<false>(x, f);
+  const float f = old * inverse(s), most = __uint_as_float(kLargest);
+  if (magnitude(old) > kMostScale) return times<true>(x, magnitude(old) <= kLargest ? fminf(fmaxf(f, -most), most) : f);
+  return times<false>(x, fminf(fmaxf(f, -most), most));
 }
 
 }  // namespace

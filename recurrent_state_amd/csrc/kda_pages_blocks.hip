@@ -241,10 +241,11 @@ __global__ void __launch_bounds__(64 * (W > 4 ? W : 4)) append_blocks_kernel(Blo
         if (joins) {
           s = max(s, power_of_two(old));
           if (s != __float_as_uint(old)) {
+            const float f = old * inverse(s);  // at most 1, but for a scale past 2^120
 #pragma unroll 1
             for (int r = part * RPP + lane / LPR; r < it.lo - it.begin; r += W * RPP) {
               codes16* const at = reinterpret_cast<codes16*>(dst + r * D + 16 * w);
-              *at = rescaled(*at, old, s);
+              *at = times<true>(*at, f);
             }
           }
         }
