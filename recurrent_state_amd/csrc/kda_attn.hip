@@ -144,25 +144,15 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
         }
       };
       // O^T += V^T P^T, with blocks' scales in the probabilities (powers of two
-      // there lose nothing).  PART: some row does not see some token; its
-      // probability stays zero, whatever the scale is.
-      auto weigh = [&](auto part) {
-        constexpr bool PART = decltype(part)::value;
-        const int g = PART ? here(lane) >> 4 : 0;
+      // there lose nothing).
+      auto weigh = [&] {
         if constexpr (BLK)
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) {
-            // The row sees token j: j - first < count, without sign.
-            const uint32_t first = a.window > 0 ? vis[n] - a.window + 1 : 0, count = vis[n] + 1 - first;
-            const uint32_t at = t0 + 4 * g - first;
+          for (int u = 0; u < GROUPS; ++u)
 #pragma unroll
-            for (int u = 0; u < GROUPS; ++u)
+            for (int n = 0; n < NQ; ++n)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float x = p[n][u][i] * v_block[u];
-                p[n][u][i] = !PART || at + 16 * u + i < count ? x : 0.f;
-              }
-          }
+              for (int i = 0; i < 4; ++i) p[n][u][i] *= v_block[u];
         cache.weigh(p, out);
       };
       // Scores to probabilities, and the earlier sums to the new maximum.
@@ -215,7 +205,7 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
           scores();
           load_k(t0 + TILE);
           softmax(std::false_type{});
-          weigh(std::false_type{});
+          weigh();
           load_v();
         }
         scores();
@@ -266,7 +256,24 @@ __global__ void __launch_bounds__(kWaves * kWave, NQ == 1 ? 3 : NQ == 2 ? 2 : 1)
             }
           }
         }
-        weigh(std::true_type{});
+        // Nor may a probability of zero meet a scale that is not finite: such a scale
+        // goes to the rows that see its group, and the group counts as scaled.
+        if constexpr (BLK)
+#pragma unroll
+          for (int u = 0; u < GROUPS; ++u) {
+            if (fabsf(v_block[u]) < INFINITY) continue;
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+              const int low = a.window > 0 ? vis[n] - a.window : -1;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int j = t0 + 16 * u + 4 * g + i;
+                if (j <= vis[n] && j > low) p[n][u][i] *= v_block[u];
+              }
+            }
+            v_block[u] = 1.f;
+          }
+        weigh();
         t0 += TILE;
       }
 
