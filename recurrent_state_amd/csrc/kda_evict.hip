@@ -324,7 +324,10 @@ struct Parts {
 // Rows are shared out where one workgroup to a row leaves most of the chip idle
 // and takes longer than four launches.  Whole calls, shared out and not: 8 rows of
 // 41000 tokens 28 and 28 us, of 57000 30 and 35, of 180000 40 and 70; 32 rows 38 and
-// 37, 40 and 45, 80 and 82; 64 rows of 57000 57 and 52, of 120000 95 and 72.
+// 37, 40 and 45, 80 and 82; 64 rows of 57000 57 and 52, of 120000 95 and 72.  The host
+// knows the table only: rows that are short in a long one lose by it (8 rows of a
+// table of 100001, of 5000 tokens 27 and 18 us, of 20000 30 and 26, of 40000 32 and
+// 32, of 60000 30 and 38).
 constexpr int kFewestParts = 6, kMostRows = 32, kMostParts = 1024;
 constexpr int kEach = kShort / kSelect;  // of a thread: every 64th of its wave's stretch
 
@@ -508,9 +511,11 @@ struct Held {
 
 // A wave takes 16 or 32 rows of a new block, keys and values together, so that many
 // loads are on their way; W waves to a block, NW to a workgroup.  16 rows leave the
-// chip more waves, but waves of a block wait for each other: of 64 sequences the
-// whole call into blocks of 32 takes 76 us with 16 rows and 78 with 32, of 64
-// 76 and 78, of 128 80 and 78.
+// chip more waves, but waves of a block wait for each other.  Whole calls with 16 and
+// 32 rows, into blocks of 32, 64, 128 and 256: 64 sequences of 500 to 8191 tokens to
+// 2000 74 and 76 us, 75 and 76, 79 and 76, 97 and 82; 8 of 4000 to 30000 to 3000 43 and
+// 44, 43 and 45, 45 and 45, 50 and 48; 256 of 300 to 1200 to 256 99 and 98, 98 and 98,
+// 97 and 98, 106 and 98; one of 30000 to 8000 30 to 32 in each.
 template <int D, int ROWS, int W>
 __global__ void __launch_bounds__(64 * (W > 4 ? W : 4)) move_blocks_kernel(EvictArgs a, int parts) {
   constexpr int NW = W > 4 ? W : 4, BLOCKS = NW / W, SHIFT = __builtin_ctz(ROWS * W);

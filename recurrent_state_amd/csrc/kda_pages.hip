@@ -218,10 +218,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
 }
 
 // Calls that touch more than the 256 MB Infinity Cache go past it: 65536 tokens
-// of 32 + 8 heads of 128 in 284 us for 288 with plain accesses, into e4m3 285 for
-// 303.  f32 and latent prompts lose by it (16384 f32 tokens 170 us for 147, 32768
-// latent ones 503 for 444).  What smaller calls write stays there for the
-// attention that reads it next.
+// of 32 + 8 heads of 128 in 282 us for 292 with plain accesses, into e4m3 283 for
+// 300; with pairs dealt to three axes 314 for 343 and 435 for 454.  The rule goes by
+// bytes alone, and f32 and latent prompts lose by it: 16384 f32 tokens 173 us for
+// 146, with axes 184 for 167; 32768 latent ones 500 for 445, with axes 567 for 493.
+// What smaller calls write stays there for the attention that reads it next.
 template <int DK, int DV, typename TIn, typename TC, bool NT, bool AXES, int HEADS>
 hipError_t run(AppendArgs a, hipStream_t st) {
   const kda_kv_shape& s = a.kb.s;
@@ -235,9 +236,19 @@ hipError_t run(AppendArgs a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Four heads to a thread (two of e4m3) where that leaves threads enough for the chip: 20000
-// tokens of 32 + 8 heads with pairs dealt to three axes 151 -> 104 us, but one
-// token 3.5 -> 4.8.
+// With axes a thread takes four heads (two into e4m3) from 2^24 values on, 2730 tokens
+// of 32 + 8 heads of 128, so that the pairs' angle rows are read once for them.  us
+// with one head to a thread, two and four, pairs dealt to three axes:
+//           2^22 values        2^23               2^24               2^26
+//   bf16     8.5  7.4  7.5     14.3 11.9 10.6     23.0 19.2 17.1     81   64   59
+//   e4m3     8.8  9.0 10.6     14.7 15.2 18.1     23.2 21.5 26.4     86   83  101
+//   f32     11.9 11.1 10.9     18.2 17.2 17.8     37.0 35.4 38.2    140  124  125
+//   latent   6.5  7.0  7.2     10.8 10.8 11.6     17.0 16.8 17.7     67   63   68
+// and by sections, where units of one axis read whole rows of angles in any case:
+//   bf16     5.8  6.0  6.8      9.7  9.4  9.4     15.4 15.7 16.1     57   55   57
+//   e4m3     6.3  7.6 10.0     10.6 13.1 17.2     16.3 18.7 25.3     62   73   96
+// Fewer values leave the chip without threads (one token 3.5 -> 4.8 with four).  The
+// rule is made for dealt pairs; sections into e4m3 lose by it.
 template <int DK, int DV, typename TIn, typename TC>
 hipError_t run(const AppendArgs& a, hipStream_t st) {
   const kda_kv_shape& s = a.kb.s;

@@ -100,8 +100,11 @@ struct Raw16 {
 // registers, and the next kind's values are asked for before this one's are used
 // (each kind's angles read anew and no loads ahead: 484 us for 300, see below).
 // Large calls are bound by memory: 8 prompts of 8192 tokens, 8 kv heads and 32 query
-// heads of 128, 1.48 GB, 300 us (4.9 TB/s; a copy of 768 MiB 5.3).  Small ones by the
-// chain of loads: lengths, page, old scale, codes.
+// heads of 128, 1.48 GB, 300 us (4.9 TB/s; a copy of 768 MiB 5.3) into blocks of 64.
+// Into blocks of 16, 32, 128 and 256 they take 260, 294, 313 and 374 us; with positions
+// on three axes, by sections and dealt to the pairs, blocks of 64 take 359 and 359, of
+// 256 414 and 694: there every head's angles are read anew.  Small calls are bound by
+// the chain of loads: lengths, page, old scale, codes.
 template <int D, int W, bool NT, bool AXES>
 __global__ void __launch_bounds__(64 * (W > 4 ? W : 4)) append_blocks_kernel(BlocksArgs a) {
   constexpr int NW = W > 4 ? W : 4, SETS = NW / W;

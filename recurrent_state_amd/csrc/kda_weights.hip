@@ -13,14 +13,21 @@
 //                        queries and lse stay in its registers: bound by the read
 //                        of the keys, and no wave waits for another.  A decode step
 //                        of 64 sequences of 60 to 8191 tokens, 8 kv heads of 128 in
-//                        bf16, 230 MB: 49 us (4.7 TB/s).
+//                        bf16, 230 MB: 49 us (4.7 TB/s); e4m3 30, with scales by blocks
+//                        29, f32 96.
 //   more                 Each wave takes a quarter of the rows, 16 or 32 at a time,
-//                        and every tile: bound by the vector instructions (busy 63 %
-//                        of the time, a third of that with exponentials; the matrix
-//                        cores 19 %).  The keys come through the LDS, and the waves'
+//                        and every tile: bound by the vector instructions (25 us of
+//                        issue at 2.4 GHz, 8 of them exponentials; the matrix cores'
+//                        work is 7).  The keys come through the LDS, and the waves'
 //                        sums meet there, every kRing tiles.  The last 32 tokens of
 //                        four prompts of 7001 to 30000, 8 kv heads of 128 in e4m3 with
-//                        128 rows each: 38 us (0.51 PFLOP/s, 74 MB).
+//                        128 rows each: 34 us (0.51 PFLOP/s, 74 MB), 38 for the first
+//                        hundred calls, until the clock has risen; bf16 39, f32 162.
+//
+// Rounding: all in fp32.  lse times log2 e is rounded once for a row, which moves its
+// weights by as much as half a step of lse itself does, and the exponential is the
+// hardware's.  Those prompts' sums are 5.4e-8 of their size from those in 64 bits, and
+// 4.1e-8 where elementary fp32 operations make them.
 
 #include <type_traits>
 
@@ -286,7 +293,7 @@ constexpr int kRowsWaves = sizeof(TIn) == 4 && D == 128 && NQ == 2 ? 3 : 4;
 
 // More rows: NQ blocks of 16 to a wave, and chunks of 64 NQ rows in turn.  The keys
 // go through the LDS, once for all four waves and three tiles ahead (read by every
-// wave into its registers, one ahead, it waited most of the time: 62 us for 38).
+// wave into its registers, one ahead, it waited most of the time: 62 us for 34).
 template <int D, typename TIn, typename TC, int NQ, bool BLK>
 __global__ void __launch_bounds__(kWaves * kWave, (kRowsWaves<D, TIn, NQ>)) rows_kernel(WeightsArgs w) {
   typedef Staged<D, TC> S;
@@ -412,7 +419,8 @@ __global__ void __launch_bounds__(kWaves * kWave, (kRowsWaves<D, TIn, NQ>)) rows
   }
 }
 
-// As many workgroups as the chip's 256 CUs hold at once.
+// As many workgroups as the chip's 256 CUs hold at once; a fourth to a CU for up to 16
+// rows costs 64 sequences 51 us for 49 (16 of them 13.2 for 14.5).
 void split(WeightsArgs& w, int tile, int at_once) {
   const Split d{tile, 0, 1, 0, 1, 1, 6};
   w.a.workers = workers_of(w.a.kb.s, 256 * at_once, d, w.a.kb.pages.page_size, w.a.kb.max_pages);
@@ -437,6 +445,18 @@ hipError_t run_rows(WeightsArgs w, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Four prompts of 7001 to 30000 tokens, us by query rows of a kv head:
+//                  16 rows  32      48      64      96      128
+//   bf16, tokens     32.1   33.2
+//         rows, 16   32.8   33.3    33.9    34.6    56.6    57.8
+//         rows, 32                  35.7    35.9    37.3    38.6
+//   e4m3 in blocks   16.8   19.0
+//         rows, 16   21.6   23.6    25.3    27.0    48.9    51.1
+//         rows, 32                  27.1    27.1    31.2    34.3
+//   f32, tokens      63.8   83.1
+//         rows, 16   58.5   70.5    87.0    98.5    179     193
+//         rows, 32                  125     125     158     162
+// So the border at 32 rows costs f32, whose operands take twice the registers.
 template <int D, typename TIn, typename TC, bool BLK>
 hipError_t by_rows(const WeightsArgs& w, hipStream_t st) {
   const kda_kv_shape& s = w.a.kb.s;
