@@ -1,4 +1,5 @@
-"""The README's loop with a budget of tokens, as it stands there: the sums of weights follow their tokens through a cut."""
+"""The serving loop with a budget of tokens that the introduction for users prints, run as it is printed: the sums of
+weights follow their tokens through a cut."""
 
 from __future__ import annotations
 
@@ -23,7 +24,7 @@ def kda():
     return k
 
 
-def loop_of_the_readme():
+def printed_loop():
     """The indented lines after the paragraph on budgets."""
     with open(os.path.join(ROOT, "README.md")) as f:
         lines = f.read().split("A budget of tokens for each head", 1)[1].split("\n")
@@ -45,7 +46,7 @@ def test_sums_go_on_after_a_cut(kda):
              new_weights=torch.full((B, Hkv, wide * page), 7.0, device=dev),
              kept=torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev))
     x["ws"] = kda.attn_workspace(x["pool"], x["table"], Hq=Hq, T=T)
-    loop = loop_of_the_readme()
+    loop = printed_loop()
     sums, tol, at = np.zeros((B, Hkv, wide * page)), np.zeros((B, Hkv, wide * page)), x["length"].clone()
     for step in range(13):
         x["q"], x["k"], x["v"] = (torch.randn((B, T, h, d), device=dev, generator=g).bfloat16() for h in (Hq, Hkv, Hkv))
